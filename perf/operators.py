@@ -426,9 +426,13 @@ def _own(s):
     if op == "grouped_grad":
         return [sbn.bitlinear_grouped_grad_x(s["dy"], s["offsets"], _weights(s, sbn)),
                 sbn.bitlinear_grouped_grad_w(s["dy"], s["xq"], s["xs"], s["offsets"])]
-    q = s["parts"]
-    sbn.adamw(q["p"], q["g"], q["m"], q["v"], s["step"], lr=LR, betas=(BETA1, BETA2), eps=EPS, weight_decay=DECAY,
-              m_scales=q.get("ms"), v_scales=q.get("vs"), copies=q.get("copy"), seed=SEED)
+    if "handle" not in s:
+        q = s["parts"]
+        s["handle"] = opt = sbn.AdamW(q["p"], lr=LR, betas=(BETA1, BETA2), eps=EPS, weight_decay=DECAY,
+                                      state_bits=s["bits"], copies=q.get("copy"), seed=SEED)
+        opt.m, opt.v, opt.m_scales, opt.v_scales = q["m"], q["v"], q.get("ms"), q.get("vs")
+        opt.step_state = s["step"]
+    s["handle"].step(s["parts"]["g"])
     return _adamw_out(s)
 
 
