@@ -347,16 +347,20 @@ def _power(e):
     return ((e + 127) << 23).view(F32)
 
 
-def _state8(x, u, lift=False):
-    """x -> e4m3 codes and one power of two per block of 256, rounded up with
-    the probability of the remainder (u uniform in [0, 1)); lift: no positive
-    value becomes zero."""
+def _state8(x, u, root=False):
+    """x -> e4m3 codes and one power of two per block of 256. Between two codes
+    n and n + 1 (in steps of the grid at x) the upper one is taken with the
+    probability that keeps x in expectation, or its square for a root, of which
+    no positive value becomes zero; u is uniform in [0, 1)."""
     top = x.abs().view(-1, BLOCK).amax(dim=1)
     e = torch.clamp((top.view(torch.int32) >> 23) - 127, min=-100)
     y = (x.abs().view(-1, BLOCK) * _power(7 - e)[:, None]).view(-1)
     ey = torch.clamp((y.view(torch.int32) >> 23) - 127, min=-6)
-    q = torch.floor(y * _power(3 - ey) + u) * _power(ey - 3)
-    if lift:
+    steps = y * _power(3 - ey)
+    n = torch.floor(steps)
+    up = u * (n + n + 1) < (steps - n) * (steps + n) if root else u < steps - n
+    q = (n + up.float()) * _power(ey - 3)
+    if root:
         q = torch.where(y > 0, torch.clamp(q, min=2.0**-9), q)
     return torch.copysign(q, x).to(torch.float8_e4m3fn), _power(e - 7)
 
@@ -384,7 +388,7 @@ def _plain_adamw(s):
         key = _mix((SEED + s["step"][0].long() * HASH_A + s["tensor"] * HASH_B) & 0xFFFFFFFF)
         h = _mix((s["index"].long().view(-1, BLOCK) ^ key[:, None]).view(-1))
         m8, ms = _state8(m, (h & 0xFFFF).float() * 2.0**-16)
-        v8, vs = _state8(r, (h >> 16).float() * 2.0**-16, lift=True)
+        v8, vs = _state8(r, (h >> 16).float() * 2.0**-16, root=True)
         s["m"].copy_(m8)
         s["ms"].copy_(ms)
         s["v"].copy_(v8)
