@@ -430,6 +430,60 @@ sbn_status sbn_bitlinear_grad_w(const void* dy_bf16, const int8_t* xq,
                                 int32_t n_out, void* dw_bf16, void* stream);
 
 /*
+ * sbn_adamw -- one AdamW step over many tensors in one launch (decoupled
+ * weight decay; "Sparse-BitNet ..." Table 5 trains the latent weights with
+ * it). With t = step[0] + 1, per element, every operation rounded in fp32:
+ *     m = b1 m + (1 - b1) g        v = b2 v + (1 - b2) g^2
+ *     p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * and step[0] = t afterwards (on the device, so the call can be captured into
+ * a CUDA graph and replayed).
+ *
+ *   tensors       host array of `count` entries, read during the call; the
+ *                 pointers in it are device memory, aligned to their type.
+ *     p           fp32 (p_bf16 = 0) or bf16 parameters, updated.
+ *     g           fp32 (g_bf16 = 0) or bf16 gradients, read.
+ *     m, v        state_bits = 32: fp32 averages of g and g^2, updated.
+ *                 state_bits = 8: e4m3 codes of m and of r = sqrt(v), one
+ *                 byte per element, with one power of two per block of 256
+ *                 consecutive elements of the tensor in m_scale and v_scale
+ *                 (fp32, ceil(numel / 256) each): m = code * scale,
+ *                 v = (code * scale)^2. Codes round up with the probability that
+ *                 keeps the expectation of m and of v, from a hash of (seed, t,
+ *                 index of the tensor in the call, index of the element); a
+ *                 positive r never becomes 0. All-zero codes with any finite
+ *                 scales are the state before the first step.
+ *     copy_bf16   optional (p_bf16 = 0): bf16 copy of the updated p, the
+ *                 input of sbn_quantize_weights.
+ *     numel       elements, 0 <= numel < 2^31. No two entries may overlap.
+ *   step          device, int32 [2]: completed steps, and a word of the
+ *                 library that is zero between calls. Calls that share it
+ *                 must not overlap in time.
+ *   lr, lr_dev    the learning rate, from the device word lr_dev if not NULL.
+ *   grad_scale    optional device word: the gradients are multiplied by it first.
+ * Errors: SBN_ERR_NULL, SBN_ERR_SHAPE (count, numel, state_bits, betas
+ * outside [0, 1), eps below 0, a copy of bf16 parameters), SBN_ERR_ALIGN
+ * (before anything is enqueued); SBN_ERR_CUDA.
+ */
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy_bf16;
+  int64_t numel;
+} sbn_adamw_tensor;
+
+#define SBN_ADAMW_BLOCK 256
+
+sbn_status sbn_adamw(const sbn_adamw_tensor* tensors, int32_t count, int32_t p_bf16,
+                     int32_t g_bf16, int32_t state_bits, int32_t* step, double lr,
+                     const float* lr_dev, double beta1, double beta2, double eps,
+                     double weight_decay, const float* grad_scale, uint32_t seed,
+                     void* stream);
+
+/*
  * Measurement helper (no counterpart in the method): the INT8 rate of the
  * tensor pipe. Launches one CTA per SM on `stream`, each issuing `iters`
  * back-to-back tcgen05.mma kind::i8 instructions of M = 128, N = 256,

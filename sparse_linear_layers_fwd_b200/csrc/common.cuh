@@ -13,9 +13,9 @@ namespace sbn {
 // Error word: one per device, set by bounded waits that give up.
 // ---------------------------------------------------------------------------
 enum : unsigned { kDevErrNone = 0u, kDevErrTimeout = 1u };
-// The library is one translation unit (sbn.cu includes every kernel header),
-// so the word is defined here, once.
-__device__ unsigned int g_dev_error;
+// Every translation unit has its own word (device code is not linked across
+// units); sbn_get_device_error reads and clears them all.
+static __device__ unsigned int g_dev_error;
 
 // Nanoseconds of the GPU's global timer (for waits bounded in time).
 SBN_DEVFN unsigned long long global_ns() {

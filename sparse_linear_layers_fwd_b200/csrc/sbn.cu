@@ -8,13 +8,12 @@
 #include "sbn.h"
 
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <cstring>
-#include <utility>
 
 #include "common.cuh"
+#include "host.cuh"
 #include "qa.cuh"
 #include "qw.cuh"
 #include "qw_fused.cuh"
@@ -35,109 +34,9 @@
 #include "bl_tc.cuh"
 #include "probe.cuh"
 
-#include <cudaTypedefs.h>
-
 namespace sbn {
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-int g_dev_checked[kMaxDevices];  // 0 unknown, 1 ok, -1 unsupported
-int g_dev_sms[kMaxDevices];
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
-
-bool pattern_ok(int n, int m) {
-  return (m == 4 || m == 8 || m == 16) && n >= 1 && n <= m && (4 * n) % m == 0;
-}
-
-bool prod_lt_2_31(long long a, long long b) { return a >= 0 && b >= 0 && a * b < (1ll << 31); }
-
-size_t round_up16(size_t x) { return (x + 15u) & ~size_t(15); }
-
-// Current device must be an sm_100 part (the library carries sm_100a code only).
-sbn_status check_device(int* dev_out, int* sms_out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return SBN_ERR_CUDA; }
-  if (dev < 0 || dev >= kMaxDevices) return SBN_ERR_DEVICE;
-  if (g_dev_checked[dev] == 0) {
-    int major = 0, sms = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return SBN_ERR_CUDA;
-    }
-    g_dev_sms[dev] = sms;
-    g_dev_checked[dev] = (major == 10) ? 1 : -1;
-  }
-  if (g_dev_checked[dev] < 0) return SBN_ERR_DEVICE;
-  *dev_out = dev;
-  *sms_out = g_dev_sms[dev];
-  return SBN_OK;
-}
-
-sbn_status launch_status() {
-  return cudaGetLastError() == cudaSuccess ? SBN_OK : SBN_ERR_CUDA;
-}
-
-// Programmatic dependent launch of the kernels that call griddep_wait()
-// before touching global memory: each may be scheduled while the previous
-// grid on the stream is finishing, so its launch and set-up (barriers,
-// TMEM, selector tables) overlap that grid's tail. Switched by
-// sbn_set_programmatic_launch; on by default.
-std::atomic<int> g_pdl{1};
-
-// The dynamic shared-memory limit of a kernel, raised once per device (flags:
-// one per device, owned by the caller's instantiation).
-template <typename K>
-bool set_smem_attr_once(K kern, size_t bytes, bool* flags) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return false;
-  }
-  if (!flags[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return false;
-    }
-    flags[dev] = true;
-  }
-  return true;
-}
-
-// cudaLaunchKernelEx with the programmatic attribute (when switched on) and,
-// for cluster > 1, clusters of `cluster` CTAs along x.
-template <typename... KArgs, typename... Args>
-sbn_status launch_ex(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                     unsigned cluster, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  unsigned na = 0;
-  if (g_pdl.load(std::memory_order_relaxed)) {
-    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[na].val.programmaticStreamSerializationAllowed = 1;
-    ++na;
-  }
-  if (cluster > 1) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = cluster;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = na;
-  if (cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) != cudaSuccess) {
-    cudaGetLastError();
-    return SBN_ERR_CUDA;
-  }
-  return SBN_OK;
-}
 
 sbn_status validate_weights_shape(int32_t n_out, int32_t k, int32_t n, int32_t m) {
   if (!pattern_ok(n, m)) return SBN_ERR_PATTERN;
@@ -390,22 +289,6 @@ sbn_status dispatch_decode_ent(const DresParams& p, int n, int m, int grid, size
     case 8 * 8 + 3: return launch_decode_ent<8, 3, NT, ACC, XBF>(p, grid, smem, st);
   }
   return SBN_ERR_PATTERN;
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
 }
 
 template <int MM, int CB, bool DENSE, bool ACC>

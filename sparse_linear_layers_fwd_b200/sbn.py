@@ -11,11 +11,13 @@ fallback: if ``libsbn.so`` is missing, loading it raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +70,9 @@ PROTOTYPES = {
     "sbn_bitlinear_grad_x": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p,
                                             _c_p, _c_p]),
     "sbn_bitlinear_grad_w": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_p, _c_p]),
+    "sbn_adamw": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, ctypes.c_double, _c_p,
+                                 ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _c_p,
+                                 ctypes.c_uint32, _c_p]),
     "sbn_probe_i8_mma": (ctypes.c_int, [_c_i32, ctypes.POINTER(ctypes.c_int32), _c_p]),
     "sbn_probe_i8_sparse_mma": (ctypes.c_int, [_c_i32, ctypes.POINTER(ctypes.c_int32), _c_p]),
     "sbn_selftest_wait_timeout": (ctypes.c_int, [_c_i32, ctypes.c_int64, _c_p]),
@@ -124,6 +129,41 @@ def _need(t: torch.Tensor, dtype, what: str):
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
+
+
+def _one_device(*tensors) -> torch.device:
+    """The device of the tensors (None entries skipped); all must share it."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+def _run_on(dev: torch.device, name: str, stream, *args):
+    """Call entry point `name` with the stream appended, on the device of its
+    tensors (made current for the call when another one is)."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream_ptr(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream_ptr(stream)), name)
+
+
+def _alloc_on(dev: torch.device, stream):
+    """Scope in which outputs and workspaces of a call on `stream` are allocated:
+    memory belongs to the stream that uses it, so that it is not handed out
+    again while the call still runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
 
 
 @dataclass
@@ -428,6 +468,136 @@ def bitlinear_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor,
     st = lib().sbn_bitlinear_grad_w(_ptr(dy), _ptr(xq), _ptr(s), t, k, n_out, _ptr(out), _stream_ptr(stream))
     _check(st, "sbn_bitlinear_grad_w")
     return out
+
+
+ADAMW_BLOCK = 256   # SBN_ADAMW_BLOCK: elements that share a scale in the 8-bit states
+
+
+class AdamW:
+    """sbn_adamw: AdamW over a list of tensors, one launch per step.
+
+        opt = AdamW(masters, lr=1e-3, state_bits=8, copies=latent_bf16)
+        opt.step(grads)
+
+    params: contiguous CUDA tensors, all fp32 or all bf16. copies (fp32
+    parameters only): bf16 tensors that receive the updated parameters, the
+    latent weights quantize_weights reads. state_bits: 32 keeps m and v in
+    fp32; 8 keeps m and sqrt(v) as float8_e4m3fn codes with one power of two
+    per 256 elements, rounded stochastically from `seed`, the step, the position
+    of the tensor in the list and the index of the element.
+
+    The state lives in m, v, m_scales, v_scales (lists, in the order of
+    params) and step (int32 [2] on the device: completed steps and a word of
+    the library); state_dict() / load_state_dict() copy it. lr is a float, or
+    an fp32 device tensor of one element that a captured graph reads anew at
+    every replay.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, betas=(0.9, 0.95), eps: float = 1e-5,
+                 weight_decay: float = 0.1, state_bits: int = 32,
+                 copies: Optional[Sequence[torch.Tensor]] = None, seed: int = 0):
+        self.params = list(params)
+        self.copies = None if copies is None else list(copies)
+        if not self.params:
+            raise ValueError("no parameters")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits, self.seed = state_bits, seed
+        dt = self.params[0].dtype
+        if dt not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"parameters must be float32 or bfloat16, got {dt}")
+        for p in self.params:
+            _need(p, dt, "params")
+        self.device = _one_device(*self.params)
+        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(1 for p in self.params if p.numel()):
+            raise ValueError("a parameter appears twice")
+        if self.copies is not None:
+            if dt != torch.float32:
+                raise TypeError("copies go with float32 parameters")
+            if len(self.copies) != len(self.params):
+                raise ValueError("copies and params differ in length")
+            for p, c in zip(self.params, self.copies):
+                _need(c, torch.bfloat16, "copies")
+                if c.numel() != p.numel():
+                    raise ValueError("a copy and its parameter differ in size")
+            _one_device(self.params[0], *self.copies)
+        kw = dict(device=self.device)
+        st = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        self.m = [torch.zeros(p.numel(), dtype=st, **kw) for p in self.params]
+        self.v = [torch.zeros(p.numel(), dtype=st, **kw) for p in self.params]
+        self.m_scales = self.v_scales = None
+        if state_bits == 8:
+            blocks = [-(-p.numel() // ADAMW_BLOCK) for p in self.params]
+            self.m_scales = [torch.ones(b, dtype=torch.float32, **kw) for b in blocks]
+            self.v_scales = [torch.ones(b, dtype=torch.float32, **kw) for b in blocks]
+        self.step_state = torch.zeros(2, dtype=torch.int32, **kw)
+        # entries of sbn_adamw_tensor, eight 64-bit words each; the gradient
+        # pointers are filled in by step()
+        self._table = np.zeros((len(self.params), 8), dtype=np.int64)
+
+    def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+        """One step with the gradients of params (same order and sizes, all
+        bf16 or all fp32, contiguous). grad_scale: fp32 device tensor of one
+        element that multiplies every gradient first."""
+        if len(grads) != len(self.params):
+            raise ValueError("grads and params differ in length")
+        gd = grads[0].dtype
+        if gd not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"grads must be float32 or bfloat16, got {gd}")
+        for g, p in zip(grads, self.params):
+            if g.dtype != gd or g.device != self.device or not g.is_contiguous() or g.numel() != p.numel():
+                _need(g, gd, "grads")
+                raise ValueError("a gradient differs from its parameter in size or device")
+            if p.device != self.device or not p.is_contiguous():
+                raise ValueError("a parameter has been moved since the optimizer was made")
+        lr_dev = None
+        lr = self.lr
+        for t, what in ((lr if isinstance(lr, torch.Tensor) else None, "lr"), (grad_scale, "grad_scale")):
+            if t is not None:
+                _need(t, torch.float32, what)
+                if t.numel() != 1:
+                    raise ValueError(f"{what} must have one element")
+                _one_device(self.params[0], t)
+        if isinstance(lr, torch.Tensor):
+            lr_dev, lr = lr, 0.0
+        tab = self._table
+        tab[:, 0] = [p.data_ptr() for p in self.params]
+        tab[:, 1] = [g.data_ptr() for g in grads]
+        tab[:, 2] = [t.data_ptr() for t in self.m]
+        tab[:, 3] = [t.data_ptr() for t in self.v]
+        if self.state_bits == 8:
+            tab[:, 4] = [t.data_ptr() for t in self.m_scales]
+            tab[:, 5] = [t.data_ptr() for t in self.v_scales]
+        if self.copies is not None:
+            tab[:, 6] = [t.data_ptr() for t in self.copies]
+        tab[:, 7] = [p.numel() for p in self.params]
+        _run_on(self.device, "sbn_adamw", stream, tab.ctypes.data, len(self.params),
+                int(self.params[0].dtype == torch.bfloat16), int(gd == torch.bfloat16), self.state_bits,
+                _ptr(self.step_state), float(lr), _ptr(lr_dev), float(self.betas[0]), float(self.betas[1]),
+                float(self.eps), float(self.weight_decay), _ptr(grad_scale), int(self.seed) & 0xFFFFFFFF)
+
+    def _state(self):
+        names = ("m", "v") + (("m_scales", "v_scales") if self.state_bits == 8 else ())
+        return {n: getattr(self, n) for n in names}
+
+    def state_dict(self) -> dict:
+        """Copies of the state (the parameters and their copies are the caller's)."""
+        d = {n: [t.clone() for t in ts] for n, ts in self._state().items()}
+        d["step"] = self.step_state.clone()
+        d["state_bits"] = self.state_bits
+        return d
+
+    def load_state_dict(self, d: dict) -> None:
+        if d["state_bits"] != self.state_bits:
+            raise ValueError("the state has other state_bits")
+        for n, ts in self._state().items():
+            if [t.shape for t in d[n]] != [t.shape for t in ts]:
+                raise ValueError("the state belongs to other parameters")
+        for n, ts in self._state().items():
+            for t, src in zip(ts, d[n]):
+                t.copy_(src)
+        self.step_state.copy_(d["step"])
 
 
 def set_programmatic_launch(enable: bool) -> bool:
