@@ -430,6 +430,110 @@ sbn_status sbn_bitlinear_grad_w(const void* dy_bf16, const int8_t* xq,
                                 int32_t n_out, void* dw_bf16, void* stream);
 
 /*
+ * Epilogue of the layer: bias, activation, residual (a feed-forward block's
+ * own steps after the rescaling, "The BitLinear Layer" (octagono page), fifth
+ * operation). Evaluated in fp32 on the accumulators, one rounding to bf16:
+ *     z = acc * gamma * s_t / 127 + bias      y = f(z) + residual
+ */
+#define SBN_ACT_NONE 0   /* f(z) = z */
+#define SBN_ACT_RELU 1   /* max(z, 0) */
+#define SBN_ACT_RELU2 2  /* max(z, 0)^2 */
+#define SBN_ACT_SILU 3   /* z / (1 + exp(-z)) */
+#define SBN_ACT_GELU 4   /* z Phi(z), Phi the normal distribution function */
+
+/*
+ * sbn_bitlinear_act, sbn_bitlinear_x_act -- sbn_bitlinear and
+ * sbn_bitlinear_x with the epilogue.
+ *   xq .. gamma    as for sbn_bitlinear (x_bf16, xq, x_scale as for
+ *                  sbn_bitlinear_x, whose workspace size applies).
+ *   bias           optional device fp32 [n_out].
+ *   act            one of SBN_ACT_*.
+ *   residual_bf16  optional device [t, n_out]; may be y_bf16 itself.
+ *   z_bf16         optional device output [t, n_out]: z, for sbn_act_grad. No
+ *                  other array of the call.
+ *   workspace      as for sbn_bitlinear / sbn_bitlinear_x.
+ * Errors: as sbn_bitlinear; SBN_ERR_SHAPE for an unknown act.
+ */
+sbn_status sbn_bitlinear_act(const int8_t* xq, const float* x_scale, int32_t t,
+                             int32_t k, int32_t n_out, int32_t n, int32_t m,
+                             const uint8_t* codes, const uint8_t* meta,
+                             const float* gamma, const float* bias, int32_t act,
+                             const void* residual_bf16, void* z_bf16, void* y_bf16,
+                             void* workspace, size_t ws_bytes, void* stream);
+sbn_status sbn_bitlinear_x_act(const void* x_bf16, int32_t t, int32_t k,
+                               int32_t n_out, int32_t n, int32_t m,
+                               const uint8_t* codes, const uint8_t* meta,
+                               const float* gamma, const float* bias, int32_t act,
+                               const void* residual_bf16, void* z_bf16, void* y_bf16,
+                               int8_t* xq, float* x_scale, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * sbn_act_grad -- backward of the epilogue: dz = dy f'(z) (bf16, may be dy_bf16
+ * itself) and, if dbias is not NULL, the column sums of the unrounded dz in
+ * fp32 (the same bits every time). The residual's gradient is dy itself; dx and
+ * dw follow from dz by the layer's gradients.
+ *   rows, offsets, as for the grouped calls below, with dbias [experts, n_out]
+ *   experts        (zero for an expert without rows); offsets NULL: one group
+ *                  of all rows (experts = 1).
+ * relu and relu2 take the derivative 0 at 0. Errors: SBN_ERR_NULL,
+ * SBN_ERR_SHAPE, SBN_ERR_ALIGN; SBN_ERR_CUDA.
+ */
+sbn_status sbn_act_grad(const void* dy_bf16, const void* z_bf16, int32_t rows,
+                        const int32_t* offsets, int32_t experts, int32_t n_out,
+                        int32_t act, void* dz_bf16, float* dbias, void* stream);
+
+/*
+ * The layer grouped by expert: `experts` layers of one shape and pattern,
+ * their packed weights stacked (codes [experts, n_out, codes_row_bytes], meta
+ * likewise, gamma [experts]: the arrays sbn_quantize_weights writes for each),
+ * over rows sorted by expert.
+ *   rows     rows of the activation and output arrays.
+ *   offsets  device int32 [experts + 1], non-decreasing: expert e owns the
+ *            rows offsets[e] .. offsets[e + 1] - 1, none if they are equal. Rows
+ *            outside [offsets[0], offsets[experts]) keep what their outputs
+ *            hold. Values are clamped to [0, rows] and to be non-decreasing on
+ *            the device, so no offsets lead outside an array.
+ *   bias     optional fp32 [experts, n_out].
+ *   others   as for sbn_bitlinear_act; xq, x_scale of sbn_bitlinear_grouped_x
+ *            are optional outputs for all rows, and its workspace (16-byte
+ *            aligned, sbn_bitlinear_grouped_x_workspace_bytes) may be NULL when
+ *            both are given or rows <= 16 fit the one-kernel route.
+ * 1 <= experts <= 1024; shapes as sbn_bitlinear with t = rows.
+ * sbn_bitlinear_grouped_grad_x: dX_r = dY_r (gamma_e C_e), [rows, k] bf16.
+ * sbn_bitlinear_grouped_grad_w: dW_e = sum over e's rows of dY_r^T (Xq_r s_r /
+ * 127), [experts, n_out, k] bf16, zero for an expert without rows.
+ * Errors: SBN_ERR_NULL, SBN_ERR_SHAPE, SBN_ERR_PATTERN, SBN_ERR_ALIGN,
+ * SBN_ERR_WORKSPACE (before anything is enqueued); SBN_ERR_CUDA.
+ */
+sbn_status sbn_bitlinear_grouped(const int8_t* xq, const float* x_scale, int32_t rows,
+                                 const int32_t* offsets, int32_t experts, int32_t k,
+                                 int32_t n_out, int32_t n, int32_t m,
+                                 const uint8_t* codes, const uint8_t* meta,
+                                 const float* gamma, const float* bias, int32_t act,
+                                 const void* residual_bf16, void* z_bf16, void* y_bf16,
+                                 void* stream);
+sbn_status sbn_bitlinear_grouped_x(const void* x_bf16, int32_t rows,
+                                   const int32_t* offsets, int32_t experts, int32_t k,
+                                   int32_t n_out, int32_t n, int32_t m,
+                                   const uint8_t* codes, const uint8_t* meta,
+                                   const float* gamma, const float* bias, int32_t act,
+                                   const void* residual_bf16, void* z_bf16, void* y_bf16,
+                                   int8_t* xq, float* x_scale, void* workspace,
+                                   size_t ws_bytes, void* stream);
+size_t sbn_bitlinear_grouped_x_workspace_bytes(int32_t rows, int32_t k);
+sbn_status sbn_bitlinear_grouped_grad_x(const void* dy_bf16, int32_t rows,
+                                        const int32_t* offsets, int32_t experts,
+                                        int32_t k, int32_t n_out, int32_t n, int32_t m,
+                                        const uint8_t* codes, const uint8_t* meta,
+                                        const float* gamma, void* dx_bf16, void* stream);
+sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq,
+                                        const float* x_scale, int32_t rows,
+                                        const int32_t* offsets, int32_t experts,
+                                        int32_t k, int32_t n_out, void* dw_bf16,
+                                        void* stream);
+
+/*
  * sbn_adamw -- one AdamW step over many tensors in one launch (decoupled
  * weight decay; "Sparse-BitNet ..." Table 5 trains the latent weights with
  * it). With t = step[0] + 1, per element, every operation rounded in fp32:

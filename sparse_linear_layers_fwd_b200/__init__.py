@@ -8,7 +8,9 @@ use of a binding name does, and fails loudly if the library is missing.
 
 __all__ = [
     "quantize_weights", "quantize_acts", "bitlinear", "bitlinear_acc32",
-    "Pattern", "PackedWeights", "BitLinear", "SbnError",
+    "bitlinear_act", "bitlinear_x_act", "act_grad", "quantize_experts", "bitlinear_grouped", "bitlinear_grouped_x",
+    "bitlinear_grouped_grad_x", "bitlinear_grouped_grad_w", "AdamW",
+    "Pattern", "PackedWeights", "PackedExperts", "BitLinear", "SbnError",
 ]
 
 

@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsbn.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("sbn.cu", "adamw.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("sbn.cu", "grouped.cu", "grads.cu", "adamw.cu")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 

@@ -1,0 +1,133 @@
+// Backward of the layer's epilogue: dz = dy f'(z) and the bias gradient, the
+// column sums of dz (per expert where the rows are grouped).
+//
+// Bound by DRAM: dy and z are read and dz is written once, 6 bytes per
+// element. A cluster of eight CTAs owns 128 columns of one expert's rows: 16
+// lanes of eight columns (16-byte accesses) by 16 row lanes per CTA, so 128
+// rows are in work at a time. The column sums stay in registers (fp32, of
+// the unrounded dz), then go through shared memory and the cluster's
+// distributed shared memory in a fixed order: no workspace, no atomics, the
+// same sums every time. Where N_out is not a multiple of 8 a lane takes
+// every 16th column with 2-byte accesses.
+#pragma once
+
+#include "common.cuh"
+#include "epi.cuh"
+#include "grp.cuh"
+#include "pair.cuh"
+
+namespace sbn {
+
+constexpr int kAgThreads = 256;
+constexpr int kAgCols = 128;       // columns per cluster
+constexpr int kAgCluster = 8;
+constexpr int kAgLanes = 16;       // row lanes per CTA
+constexpr int kAgUnroll = 4;       // rows of a lane in flight
+
+struct AgParams {
+  const uint16_t* dy;
+  const uint16_t* z;
+  uint16_t* dz;    // may be dy: a thread reads its elements before it writes them
+  float* dbias;     // [E, N] or NULL
+  GrpParams grp;
+  int N;
+  int act;
+};
+
+// Grid (clusters of column blocks x 8, experts).
+template <bool VEC>
+__global__ void __launch_bounds__(kAgThreads)
+act_grad_kernel(const AgParams p) {
+  __shared__ float s_sum[kAgLanes][kAgCols];
+  __shared__ float s_cta[kAgCols];
+  const int tid = threadIdx.x, lane_r = tid >> 4, lane_c = tid & 15;
+  const int rank = (int)cluster_rank();
+  const int c0 = (int)(blockIdx.x / kAgCluster) * kAgCols;
+  const int e = (int)blockIdx.y;
+  griddep_wait();
+  int lo = 0, hi = p.grp.rows;
+  if (p.grp.offsets) {
+    lo = min(max(p.grp.offsets[e], 0), p.grp.rows);
+    hi = min(max(p.grp.offsets[e + 1], 0), p.grp.rows);
+  }
+  const int step = VEC ? 1 : kAgLanes;                       // distance between a lane's columns
+  const int col = c0 + (VEC ? 8 * lane_c : lane_c);
+  float sum[8] = {};
+  for (int r0 = lo + rank * kAgLanes + lane_r; r0 < hi; r0 += kAgUnroll * kAgCluster * kAgLanes) {
+    uint4 dv[kAgUnroll], zv[kAgUnroll];
+    float d[8], z[8];
+    if (VEC) {
+#pragma unroll
+      for (int u = 0; u < kAgUnroll; ++u) {
+        const int r = r0 + u * kAgCluster * kAgLanes;
+        if (r < hi && col < p.N) {
+          dv[u] = *reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col);
+          zv[u] = *reinterpret_cast<const uint4*>(p.z + (size_t)r * p.N + col);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAgUnroll; ++u) {
+      const int r = r0 + u * kAgCluster * kAgLanes;
+      if (r >= hi || col >= p.N) continue;
+      const size_t at = (size_t)r * p.N + col;
+      if (VEC) {
+        const uint32_t dw[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w}, zw[4] = {zv[u].x, zv[u].y, zv[u].z, zv[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[2 * j] = __uint_as_float(dw[j] << 16);
+          d[2 * j + 1] = __uint_as_float(dw[j] & 0xFFFF0000u);
+          z[2 * j] = __uint_as_float(zw[j] << 16);
+          z[2 * j + 1] = __uint_as_float(zw[j] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool ok = col + j * step < p.N;
+          d[j] = ok ? bf16_bits_to_float(p.dy[at + j * step]) : 0.f;
+          z[j] = ok ? bf16_bits_to_float(p.z[at + j * step]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] *= act_df(p.act, z[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += d[j];
+      if (VEC) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = (uint32_t)f32_to_bf16_bits(d[2 * j]) | ((uint32_t)f32_to_bf16_bits(d[2 * j + 1]) << 16);
+        *reinterpret_cast<uint4*>(p.dz + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j * step < p.N) p.dz[at + j * step] = f32_to_bf16_bits(d[j]);
+      }
+    }
+  }
+  griddep_launch_dependents();
+  if (!p.dbias) return;   // the same for every CTA of the cluster
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_sum[lane_r][col - c0 + j * step] = sum[j];
+  __syncthreads();
+  if (tid < kAgCols) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAgLanes; ++i) t += s_sum[i][tid];
+    s_cta[tid] = t;
+  }
+  cluster_sync_all();
+  if (rank == 0 && tid < kAgCols && c0 + tid < p.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int c = 0; c < kAgCluster; ++c) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(smem_u32(&s_cta[tid]), (uint32_t)c)));
+      t += v;
+    }
+    p.dbias[(size_t)e * p.N + c0 + tid] = t;
+  }
+  cluster_sync_all();   // no CTA leaves while its sums are read
+}
+
+}  // namespace sbn

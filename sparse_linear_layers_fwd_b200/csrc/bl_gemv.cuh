@@ -184,8 +184,9 @@ SBN_DEVFN uint32_t gv_field(const uint32_t (&w)[NW]) {
 
 // Eight positions (group I of the thread's span) of one row -> int8 bytes
 // 0-3 (w0) and 4-7 (w1). cw: the span's code words; mw: its 8 keep bytes;
-// s_sel2: the selector pairs of the 256 keep masks.
-template <int MM, int CB, bool DENSE, int I>
+// s_sel2: the selector pairs of the 256 keep masks, COPIES of each in a row
+// (a reader with its own copy meets fewer bank conflicts).
+template <int MM, int CB, bool DENSE, int I, int COPIES = 1>
 SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* s_sel2, uint32_t& w0,
                          uint32_t& w1) {
   if constexpr (DENSE) {
@@ -203,7 +204,7 @@ SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], cons
     const uint32_t m8 = gv_prmt(mw[I / 4], 0u, 0x4440u | (I % 4));
     const uint32_t ev = gv_prmt(kCodeByteTable, 0u, gv_field<kOff, kMask, CB>(cw));
     const uint32_t od = gv_prmt(kCodeByteTable, 0u, gv_field<kOff + 2, kMask, CB>(cw));
-    const uint2 sel = s_sel2[m8];
+    const uint2 sel = s_sel2[m8 * COPIES];
     w0 = gv_prmt(ev, od, sel.x);
     w1 = gv_prmt(ev, od, sel.y);
     return;
@@ -222,7 +223,7 @@ SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], cons
     const uint32_t m8 = gv_prmt(mw[I / 4], 0u, 0x4440u | (I % 4));
     uint32_t ev, od;
     gv_codes_eo(v, ev, od);
-    const uint2 sel = s_sel2[m8];
+    const uint2 sel = s_sel2[m8 * COPIES];
     w0 = gv_prmt(ev, od, sel.x);
     w1 = gv_prmt(ev, od, sel.y);
   }

@@ -62,6 +62,8 @@
 #include "bl_tc.cuh"
 #include "bl_tc_sp.cuh"
 #include "common.cuh"
+#include "epi_tile.cuh"
+#include "pair.cuh"
 
 namespace sbn {
 
@@ -94,80 +96,6 @@ struct T2Cfg {
   static_assert(SPARSE || 2 * BN <= (int)kT2TmemCols, "accumulators must fit in TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
-
-SBN_DEVFN void tma_prefetch_map(const CUtensorMap* tmap) {
-  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
-}
-SBN_DEVFN uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return r;
-}
-// shared::cluster address of the same shared-memory offset in CTA `rank`
-SBN_DEVFN uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-SBN_DEVFN void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-SBN_DEVFN void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
-}
-// TMA tile load into this CTA's shared memory whose completion counts on an
-// mbarrier of either CTA of the pair (cluster address)
-SBN_DEVFN void tma_load_2d_pair(void* smem_dst, const CUtensorMap* tmap, int x, int y, uint32_t mbar_cluster) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(mbar_cluster)
-      : "memory");
-}
-// TMA tile store from this CTA's shared memory (elements outside the tensor
-// are not written), and the waits on this thread's outstanding stores
-SBN_DEVFN void tma_store_2d(const CUtensorMap* tmap, int x, int y, const void* smem_src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
-                   reinterpret_cast<uint64_t>(tmap)),
-               "r"(x), "r"(y), "r"(smem_u32(smem_src))
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
-}
-// at most one store group still reading its shared-memory source
-SBN_DEVFN void tma_store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory"); }
-SBN_DEVFN void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
-// arrives once on the barrier at this offset in both CTAs when every prior
-// tcgen05 operation of this thread has completed
-SBN_DEVFN void tc_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "{\n.reg .b16 msk;\nmov.b16 msk, 3;\n"
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], msk;\n}\n" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-// tcgen05.ld of 32 columns without the wait, and the wait that makes the
-// registers valid (they are in/out operands of the wait, so no use of them
-// can be scheduled before it)
-SBN_DEVFN void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-SBN_DEVFN void tmem_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
 
 template <bool SPARSE, uint32_t IDESC>
 SBN_DEVFN void tc_mma_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t tmem_e, uint32_t accumulate) {
@@ -213,11 +141,13 @@ SBN_DEVFN void tc_cp_meta_pair(uint32_t taddr, uint64_t sdesc) {
 // 128 bytes; tmap_y: the bf16 output, boxes of 32 tokens x 32 rows, used when
 // y_tma != 0 (every output row starts on a 16-byte boundary). Launched in
 // clusters of two CTAs; gridDim.x even.
-template <bool SPARSE, bool ACC, bool NARROW>
+// EPI: the layer's epilogue (epi_tile.cuh) on each chunk, with tmap_z the map
+// of z like tmap_y.
+template <bool SPARSE, bool ACC, bool NARROW, bool EPI = false>
 __global__ void __launch_bounds__(kT2Threads, 1)
 bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
               const __grid_constant__ CUtensorMap tmap_e, const __grid_constant__ CUtensorMap tmap_y,
-              const TcParams p, const int y_tma) {
+              const TcParams p, const int y_tma, const __grid_constant__ CUtensorMap tmap_z, const EpiParams ep) {
   using C = T2Cfg<SPARSE, NARROW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -391,6 +321,8 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
     constexpr int NCH = (kChunks + 1) / 2;
     const int nch = c_end - c_first;
     const float g = ACC ? 0.f : __ldg(p.gamma);
+    [[maybe_unused]] EpiTile et{wbuf, 0};
+    [[maybe_unused]] const EpiOut eo{&tmap_y, &tmap_z, p.y, p.N, p.T, y_tma != 0};
     int jt = 0;
     for (int tile = pair; tile < n_tiles; tile += npairs, ++jt) {
       const int b = jt & 1;
@@ -404,6 +336,12 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
       for (int cc = 0; cc < NCH; ++cc) {
         const int my_tok = tok0 + 32 * (c_first + cc) + lane;
         scq[cc] = (ACC || cc >= nch || my_tok >= p.T) ? 0.f : __fdiv_rn(__fmul_rn(g, __ldg(p.xs + my_tok)), 127.0f);
+      }
+      uint4 res[4];
+      float bias = 0.f;
+      if constexpr (EPI) {
+        if (ep.bias && row < p.N) bias = __ldg(ep.bias + row);
+        epi_load_residual(ep, eo, row_w, tok0 + 32 * c_first, p.T, lane, res);
       }
       int got = 1;
       if (lane == 0) got = mbar_wait(&acc_full[b], (jt >> 1) & 1u) ? 1 : 0;
@@ -422,7 +360,10 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
         uint32_t(&rn)[32] = (cc & 1) ? ra : rb;
         tmem_ld_wait(r);
         if (cc + 1 < nch) tmem_ld32_issue(tmem + lane_base + (uint32_t)(b * C::BN + 32 * (c + 1)), rn);
-        if (!ACC && y_tma) {
+        if constexpr (EPI) {
+          epi_chunk(ep, eo, et, r, scq[cc], bias, row_w, tok0 + 32 * c, p.T, cc + 1 < nch ? tok0 + 32 * (c + 1) : -1,
+                    lane, res);
+        } else if (!ACC && y_tma) {
           uint16_t* buf = wbuf + (nstore & 1) * 1024;
           if (lane == 0) tma_store_wait_read1();
           __syncwarp();

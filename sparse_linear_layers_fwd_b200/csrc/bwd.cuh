@@ -101,7 +101,7 @@ bwd_dx_kernel(const uint16_t* __restrict__ dy, int t_count, int k, int n_out, co
 }
 
 // dW = dY^T (Xq s / 127). Grid (K / 64, ceil(N_out / 64)).
-__global__ void __launch_bounds__(kBwThreads)
+static __global__ void __launch_bounds__(kBwThreads)
 bwd_dw_kernel(const uint16_t* __restrict__ dy, const int8_t* __restrict__ xq, const float* __restrict__ xs,
               int t_count, int k, int n_out, uint16_t* __restrict__ dw) {
   __shared__ float s_a[kBwSlice][kBwTile];   // dY slice: [t][n]

@@ -372,7 +372,7 @@ SBN_DEVFN void s8x4_to_bf16x4_any(uint32_t q, uint32_t& lo, uint32_t& hi) {
   hi = (__float_as_uint(f2) >> 16) | (__float_as_uint(f3) & 0xFFFF0000u);
 }
 
-__global__ void __launch_bounds__(kTcThreads, 1) bwd_dw_tc_kernel(const BwParams p) {
+static __global__ void __launch_bounds__(kTcThreads, 1) bwd_dw_tc_kernel(const BwParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kBwStages * kBwStageBytes);

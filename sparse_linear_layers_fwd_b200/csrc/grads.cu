@@ -1,0 +1,101 @@
+// Host side of the grouped backward (see include/sbn.h): validation and the
+// launches.
+
+#include "sbn.h"
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "host.cuh"
+#include "bwd_grp.cuh"
+
+namespace sbn {
+
+sbn_status take_error_grad(unsigned* word) { return take_error_word(g_dev_error, word); }
+
+namespace {
+
+struct LaunchDx {
+  template <int MM, int CB, bool DENSE>
+  static sbn_status run(const uint16_t* dy, const GxParams& p, int sms, cudaStream_t st) {
+    const int r = p.grp.rows, e = p.grp.experts;
+    if (p.N % 8 != 0) {
+      const dim3 grid((unsigned)(p.K / kBwTile), (unsigned)(r / kBwTile + std::min(e, r)));
+      return launch_ex(bwd_dx_grp_plain_kernel<MM, CB, DENSE>, grid, dim3(kBwThreads), 8 * (size_t)(e + 1), st, 1, dy, p);
+    }
+    static bool attr_set[kMaxDevices] = {};
+    auto kern = bwd_dx_grp_kernel<MM, CB, DENSE>;
+    if (!set_smem_attr_once(kern, gx_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
+    CUtensorMap tm;
+    if (!encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, p.N, r, 2 * (uint64_t)p.N, kBxBK, kBxBM,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return SBN_ERR_CUDA;
+    const long long most = (long long)(r / kBxBM + std::min(e, r)) * ((p.K + kBxBN - 1) / kBxBN);
+    const int grid = (int)std::max(1LL, std::min(most, (long long)sms));
+    return launch_ex(kern, dim3((unsigned)grid), dim3(kTcThreads), gx_smem_bytes(e), st, 1, tm, p);
+  }
+};
+
+sbn_status check_grad(int rows, const int32_t* offsets, int experts, int k, int n_out) {
+  if (rows < 1 || n_out < 1 || k < 128 || (k % 128) != 0 || experts < 1 || experts > kGrpMaxExperts) return SBN_ERR_SHAPE;
+  if (!prod_lt_2_31(rows, k) || !prod_lt_2_31(n_out, k) || !prod_lt_2_31(rows, n_out) ||
+      !prod_lt_2_31(experts, n_out) || (rows + kBwTile - 1) / kBwTile + experts > 65535 ||
+      (n_out + kBwTile - 1) / kBwTile > 65535)
+    return SBN_ERR_SHAPE;
+  return (reinterpret_cast<uintptr_t>(offsets) & 3u) ? SBN_ERR_ALIGN : SBN_OK;
+}
+
+}  // namespace
+}  // namespace sbn
+
+using namespace sbn;
+
+extern "C" {
+
+sbn_status sbn_bitlinear_grouped_grad_x(const void* dy_bf16, int32_t rows, const int32_t* offsets, int32_t experts,
+                                        int32_t k, int32_t n_out, int32_t n, int32_t m, const uint8_t* codes,
+                                        const uint8_t* meta, const float* gamma, void* dx_bf16, void* stream) {
+  if (!dy_bf16 || !offsets || !codes || !gamma || !dx_bf16 || (n != m && !meta)) return SBN_ERR_NULL;
+  if (!pattern_ok(n, m)) return SBN_ERR_PATTERN;
+  sbn_status st = check_grad(rows, offsets, experts, k, n_out);
+  if (st != SBN_OK) return st;
+  if (!aligned16(dy_bf16) || !aligned16(codes) || !aligned16(meta) || !aligned16(dx_bf16) ||
+      (reinterpret_cast<uintptr_t>(gamma) & 3u))
+    return SBN_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev, &sms)) != SBN_OK) return st;
+  GxParams p;
+  p.codes = codes; p.meta = meta; p.gamma = gamma; p.dx = reinterpret_cast<uint16_t*>(dx_bf16);
+  p.grp = GrpParams{offsets, experts, rows}; p.K = k; p.N = n_out;
+  p.cstride = (int)sbn_codes_row_bytes(k, n, m); p.mstride = (int)sbn_meta_row_bytes(k, n, m);
+  return by_pattern<LaunchDx>(n, m, reinterpret_cast<const uint16_t*>(dy_bf16), p, sms,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, const float* x_scale, int32_t rows,
+                                        const int32_t* offsets, int32_t experts, int32_t k, int32_t n_out,
+                                        void* dw_bf16, void* stream) {
+  if (!dy_bf16 || !xq || !x_scale || !offsets || !dw_bf16) return SBN_ERR_NULL;
+  sbn_status st = check_grad(rows, offsets, experts, k, n_out);
+  if (st != SBN_OK) return st;
+  if (!aligned16(dy_bf16) || !aligned16(xq) || !aligned16(dw_bf16) || (reinterpret_cast<uintptr_t>(x_scale) & 3u))
+    return SBN_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev, &sms)) != SBN_OK) return st;
+  GwParams p;
+  p.dy = reinterpret_cast<const uint16_t*>(dy_bf16); p.xq = xq; p.xs = x_scale;
+  p.dw = reinterpret_cast<uint16_t*>(dw_bf16); p.grp = GrpParams{offsets, experts, rows}; p.K = k; p.N = n_out;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (n_out % 8 != 0) {
+    const dim3 grid((unsigned)(k / kBwTile), (unsigned)((n_out + kBwTile - 1) / kBwTile), (unsigned)experts);
+    return launch_ex(bwd_dw_grp_plain_kernel, grid, dim3(kBwThreads), 8 * (size_t)(experts + 1), cs, 1, p);
+  }
+  static bool attr_set[kMaxDevices] = {};
+  if (!set_smem_attr_once(bwd_dw_grp_kernel, gw_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
+  const long long tiles = (long long)experts * ((n_out + kBwBM - 1) / kBwBM) * ((k + kBwBN - 1) / kBwBN);
+  const int grid = (int)std::min(tiles, (long long)sms);
+  return launch_ex(bwd_dw_grp_kernel, dim3((unsigned)grid), dim3(kTcThreads), gw_smem_bytes(experts), cs, 1, p);
+}
+
+}  // extern "C"

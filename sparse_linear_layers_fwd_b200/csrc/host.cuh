@@ -128,6 +128,48 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// Calls F::run<m, code bytes per 16 positions, n == m> for the pattern.
+template <typename F, typename... Args>
+sbn_status by_pattern(int n, int m, Args&&... args) {
+  if (n == m) return F::template run<8, 4, true>(std::forward<Args>(args)...);
+  switch (m * 8 + 4 * n / m) {
+    case 4 * 8 + 1: return F::template run<4, 1, false>(std::forward<Args>(args)...);
+    case 4 * 8 + 2: return F::template run<4, 2, false>(std::forward<Args>(args)...);
+    case 4 * 8 + 3: return F::template run<4, 3, false>(std::forward<Args>(args)...);
+    case 8 * 8 + 1: return F::template run<8, 1, false>(std::forward<Args>(args)...);
+    case 8 * 8 + 2: return F::template run<8, 2, false>(std::forward<Args>(args)...);
+    case 8 * 8 + 3: return F::template run<8, 3, false>(std::forward<Args>(args)...);
+    case 16 * 8 + 1: return F::template run<16, 1, false>(std::forward<Args>(args)...);
+    case 16 * 8 + 2: return F::template run<16, 2, false>(std::forward<Args>(args)...);
+    case 16 * 8 + 3: return F::template run<16, 3, false>(std::forward<Args>(args)...);
+  }
+  return SBN_ERR_PATTERN;
+}
+
+// Tensor map of a row-major matrix (rows of row_bytes bytes).
+inline bool encode_2d(CUtensorMap* tm, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
+               uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t gdim[2] = {inner, rows};
+  cuuint64_t gstride[1] = {row_bytes};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t estride[2] = {1, 1};
+  return enc(tm, type, 2, const_cast<void*>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct EpiParams;   // epi.cuh
+
+// Calls across the units. quantize_acts_rows: sbn_quantize_acts after its
+// checks. run_pairs_epi: t > 16 rows through the CTA-pair kernel with the
+// epilogue, ws as for sbn_bitlinear; SBN_ERR_DEVICE before any launch where no
+// pair can be resident.
+sbn_status quantize_acts_rows(const void* x_bf16, int t, int k, int8_t* xq, float* x_scale, int sms, cudaStream_t s);
+sbn_status run_pairs_epi(const int8_t* xq, const float* xs, int t, int k, int n_out, int n, int m, const uint8_t* codes,
+                         const uint8_t* meta, const float* gamma, uint16_t* y, const EpiParams& ep, void* ws, int sms,
+                         cudaStream_t st);
+
 // Device error words of the translation units (common.cuh): each unit reads
 // its own and clears it. 0: none; a CUDA failure is reported as such.
 sbn_status take_error_grouped(unsigned* word);

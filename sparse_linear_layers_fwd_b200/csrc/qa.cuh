@@ -144,7 +144,7 @@ qa_warp_kernel(const uint4* __restrict__ x, int t, int kc, uint2* __restrict__ x
 }
 
 // Rows too long for registers: two passes over the row (the second from L2).
-__global__ void __launch_bounds__(kQaThreads)
+static __global__ void __launch_bounds__(kQaThreads)
 qa_kernel_long(const uint4* __restrict__ x, int t, int kc, uint2* __restrict__ xq, float* __restrict__ scale) {
   griddep_wait();
   griddep_launch_dependents();

@@ -457,7 +457,7 @@ sbn_status launch_tc_sp(const CUtensorMap& tm, const TcParams& p, int sms, cudaS
 
 // CTA pairs of the pair kernel that can be resident at once on this device
 // (clusters of two need both SMs in one GPC); 0 if none.
-template <bool SPARSE, bool ACC, bool NARROW = false>
+template <bool SPARSE, bool ACC, bool NARROW = false, bool EPI = false>
 int tc2_max_pairs() {
   static int cached[kMaxDevices];   // 0 unknown, else pairs + 1
   int dev = 0;
@@ -467,7 +467,7 @@ int tc2_max_pairs() {
   }
   if (cached[dev] == 0) {
     using C = T2Cfg<SPARSE, NARROW>;
-    auto kern = bl_tc2_kernel<SPARSE, ACC, NARROW>;
+    auto kern = bl_tc2_kernel<SPARSE, ACC, NARROW, EPI>;
     int pairs = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) == cudaSuccess) {
       cudaLaunchConfig_t cfg = {};
@@ -503,17 +503,18 @@ bool make_out_tensor_map(CUtensorMap* ty, const uint16_t* y, int t, int n_out) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool SPARSE, bool ACC, bool NARROW = false>
+template <bool SPARSE, bool ACC, bool NARROW = false, bool EPI = false>
 sbn_status launch_tc2(const CUtensorMap& tm, const CUtensorMap& tw, const CUtensorMap& te, const TcParams& p,
-                      int max_pairs, cudaStream_t st) {
+                      int max_pairs, cudaStream_t st, const EpiParams& ep = EpiParams{}) {
   using C = T2Cfg<SPARSE, NARROW>;
   // tile stores of the output where every row starts on a 16-byte boundary
   const bool al = !ACC && p.y && (p.N % 8) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
-  CUtensorMap ty = tm;   // unused unless y_tma
-  const int y_tma = (al && make_out_tensor_map(&ty, p.y, p.T, p.N)) ? 1 : 0;
+  CUtensorMap ty = tm, tz = tm;   // unused unless y_tma (tz: and z is wanted)
+  const int y_tma = (al && make_out_tensor_map(&ty, p.y, p.T, p.N) &&
+                     (!EPI || !ep.z || make_out_tensor_map(&tz, ep.z, p.T, p.N))) ? 1 : 0;
   const int tiles = ((p.N + 255) / 256) * ((p.T + C::BN - 1) / C::BN);
-  return launch_ex(bl_tc2_kernel<SPARSE, ACC, NARROW>, dim3(2 * std::min(tiles, max_pairs)), dim3(kT2Threads), C::SMEM,
-                   st, 2, tm, tw, te, ty, p, y_tma);
+  return launch_ex(bl_tc2_kernel<SPARSE, ACC, NARROW, EPI>, dim3(2 * std::min(tiles, max_pairs)), dim3(kT2Threads),
+                   C::SMEM, st, 2, tm, tw, te, ty, p, y_tma, tz, ep);
 }
 
 // Whether the dense pair kernel should take 128-token tiles: waves of tiles
@@ -532,12 +533,14 @@ bool tc2_narrow_pays(int t, int n_out, int wide_pairs, int narrow_pairs) {
 // 2:4 weights on the sparse tensor-core MMA: expanded once into the
 // compressed workspace for the CTA-pair kernel (ws non-NULL and pairs can
 // be resident), else inside the single-CTA kernel.
-template <bool ACC_OUT>
-sbn_status run_bitlinear_sp(const int8_t* xq, const TcParams& p, void* ws, int sms, cudaStream_t st) {
+template <bool ACC_OUT, bool EPI = false>
+sbn_status run_bitlinear_sp(const int8_t* xq, const TcParams& p, void* ws, int sms, cudaStream_t st,
+                            const EpiParams& ep = EpiParams{}) {
   CUtensorMap tm;
   sbn_status s2;
-  const int pairs = ws ? tc2_max_pairs<true, ACC_OUT>() : 0;
+  const int pairs = ws ? tc2_max_pairs<true, ACC_OUT, false, EPI>() : 0;
   if (pairs <= 0) {
+    if (EPI) return SBN_ERR_DEVICE;   // the caller takes the grouped kernel
     if ((s2 = make_act_tensor_map(&tm, xq, p.T, p.K, kSpBN)) != SBN_OK) return s2;
     return launch_tc_sp<ACC_OUT>(tm, p, sms, st);
   }
@@ -554,7 +557,26 @@ sbn_status run_bitlinear_sp(const int8_t* xq, const TcParams& p, void* ws, int s
   CUtensorMap tw, te;
   if ((s2 = make_sp_weight_maps(&tw, &te, wsp, esp, p.N, n_pad, p.K)) != SBN_OK) return s2;
   if ((s2 = make_act_tensor_map(&tm, xq, p.T, p.K, T2Cfg<true>::HALF)) != SBN_OK) return s2;
-  return launch_tc2<true, ACC_OUT>(tm, tw, te, p, pairs, st);
+  return launch_tc2<true, ACC_OUT, false, EPI>(tm, tw, te, p, pairs, st, ep);
+}
+
+// Every other pattern on CTA pairs: expanded once into the workspace, then
+// both operands by TMA.
+template <bool ACC_OUT, bool EPI = false>
+sbn_status run_bitlinear_pairs(const int8_t* xq, const TcParams& p, int n, int m, void* ws, int pairs, int sms,
+                               cudaStream_t st, const EpiParams& ep = EpiParams{}) {
+  int8_t* wd = reinterpret_cast<int8_t*>(ws);
+  CUtensorMap tm, tw;
+  sbn_status s2 = dispatch_expand(p.codes, p.meta, p.N, p.K, n, m, p.cstride, p.mstride, wd, sms, st);
+  if (s2 != SBN_OK) return s2;
+  if ((s2 = make_weight_tensor_map(&tw, wd, p.N, p.K)) != SBN_OK) return s2;
+  const int npairs = tc2_max_pairs<false, ACC_OUT, true, EPI>();
+  if (tc2_narrow_pays(p.T, p.N, pairs, npairs)) {
+    if ((s2 = make_act_tensor_map(&tm, xq, p.T, p.K, T2Cfg<false, true>::HALF)) != SBN_OK) return s2;
+    return launch_tc2<false, ACC_OUT, true, EPI>(tm, tw, tw, p, npairs, st, ep);
+  }
+  if ((s2 = make_act_tensor_map(&tm, xq, p.T, p.K, T2Cfg<false>::HALF)) != SBN_OK) return s2;
+  return launch_tc2<false, ACC_OUT, false, EPI>(tm, tw, tw, p, pairs, st, ep);
 }
 
 template <bool ACC_OUT>
@@ -597,21 +619,7 @@ sbn_status run_bitlinear(const int8_t* xq, const float* xs, int32_t t, int32_t k
   if (n == 2 && m == 4) return run_bitlinear_sp<ACC_OUT>(xq, p, ws, sms, st);
   CUtensorMap tm;
   const int pairs = ws ? tc2_max_pairs<false, ACC_OUT>() : 0;
-  if (pairs > 0) {
-    // expand once into the workspace, then TMA both operands on CTA pairs
-    int8_t* wd = reinterpret_cast<int8_t*>(ws);
-    sbn_status s2 = dispatch_expand(codes, meta, n_out, k, n, m, cstride, mstride, wd, sms, st);
-    if (s2 != SBN_OK) return s2;
-    CUtensorMap tw;
-    if ((s2 = make_weight_tensor_map(&tw, wd, n_out, k)) != SBN_OK) return s2;
-    const int npairs = tc2_max_pairs<false, ACC_OUT, true>();
-    if (tc2_narrow_pays(t, n_out, pairs, npairs)) {
-      if ((s2 = make_act_tensor_map(&tm, xq, t, k, T2Cfg<false, true>::HALF)) != SBN_OK) return s2;
-      return launch_tc2<false, ACC_OUT, true>(tm, tw, tw, p, npairs, st);
-    }
-    if ((s2 = make_act_tensor_map(&tm, xq, t, k, T2Cfg<false>::HALF)) != SBN_OK) return s2;
-    return launch_tc2<false, ACC_OUT>(tm, tw, tw, p, pairs, st);
-  }
+  if (pairs > 0) return run_bitlinear_pairs<ACC_OUT>(xq, p, n, m, ws, pairs, sms, st);
   const sbn_status st_map = make_act_tensor_map(&tm, xq, t, k);
   if (st_map != SBN_OK) return st_map;
   return dispatch_tc<ACC_OUT>(tm, p, n, m, sms, st);
@@ -890,6 +898,24 @@ static_assert(kQwWorkspaceBytes <= kNoAllocScratchBytes, "workspace exceeds the 
 void* g_noalloc_ptr[kMaxDevices];  // device address of g_noalloc_scratch, per device
 
 }  // namespace
+
+sbn_status quantize_acts_rows(const void* x_bf16, int t, int k, int8_t* xq, float* x_scale, int sms, cudaStream_t s) {
+  return launch_quantize_acts(x_bf16, t, k, xq, x_scale, sms, s);
+}
+
+sbn_status run_pairs_epi(const int8_t* xq, const float* xs, int t, int k, int n_out, int n, int m, const uint8_t* codes,
+                         const uint8_t* meta, const float* gamma, uint16_t* y, const EpiParams& ep, void* ws, int sms,
+                         cudaStream_t st) {
+  TcParams p;
+  p.codes = codes; p.meta = meta; p.xs = xs; p.gamma = gamma; p.y = y; p.acc_out = nullptr;
+  p.T = t; p.K = k; p.N = n_out;
+  p.cstride = (int)sbn_codes_row_bytes(k, n, m);
+  p.mstride = (int)sbn_meta_row_bytes(k, n, m);
+  if (n == 2 && m == 4) return run_bitlinear_sp<false, true>(xq, p, ws, sms, st, ep);
+  const int pairs = tc2_max_pairs<false, false, false, true>();
+  if (pairs <= 0) return SBN_ERR_DEVICE;
+  return run_bitlinear_pairs<false, true>(xq, p, n, m, ws, pairs, sms, st, ep);
+}
 
 static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratchBytes];
 
@@ -1392,14 +1418,11 @@ sbn_status sbn_get_device_error(void* stream) {
     cudaGetLastError();
     return SBN_ERR_CUDA;
   }
-  unsigned int v = 0u;
-  const unsigned int zero = 0u;
-  if (cudaMemcpyFromSymbol(&v, g_dev_error, sizeof(v)) != cudaSuccess ||
-      cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero)) != cudaSuccess) {
-    cudaGetLastError();
-    return SBN_ERR_CUDA;
-  }
-  return v == kDevErrNone ? SBN_OK : SBN_ERR_TIMEOUT;
+  unsigned v = 0u, v_grouped = 0u, v_grad = 0u;
+  if ((st = take_error_word(g_dev_error, &v)) != SBN_OK || (st = take_error_grouped(&v_grouped)) != SBN_OK ||
+      (st = take_error_grad(&v_grad)) != SBN_OK)
+    return st;
+  return (v | v_grouped | v_grad) == kDevErrNone ? SBN_OK : SBN_ERR_TIMEOUT;
 }
 
 }  // extern "C"

@@ -70,6 +70,21 @@ PROTOTYPES = {
     "sbn_bitlinear_grad_x": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p,
                                             _c_p, _c_p]),
     "sbn_bitlinear_grad_w": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_p, _c_p]),
+    "sbn_bitlinear_act": (ctypes.c_int, [_c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p,
+                                         _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "sbn_bitlinear_x_act": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p,
+                                           _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "sbn_act_grad": (ctypes.c_int, [_c_p, _c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p]),
+    "sbn_bitlinear_grouped": (ctypes.c_int, [_c_p, _c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                             _c_p, _c_p, _c_p, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p]),
+    "sbn_bitlinear_grouped_x": (ctypes.c_int, [_c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_p,
+                                               _c_p, _c_p, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz,
+                                               _c_p]),
+    "sbn_bitlinear_grouped_x_workspace_bytes": (_c_sz, [_c_i32, _c_i32]),
+    "sbn_bitlinear_grouped_grad_x": (ctypes.c_int, [_c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                                    _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "sbn_bitlinear_grouped_grad_w": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_p,
+                                                    _c_p]),
     "sbn_adamw": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, ctypes.c_double, _c_p,
                                  ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _c_p,
                                  ctypes.c_uint32, _c_p]),
@@ -467,6 +482,287 @@ def bitlinear_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor,
         out = torch.empty((n_out, k), dtype=torch.bfloat16, device=dy.device)
     st = lib().sbn_bitlinear_grad_w(_ptr(dy), _ptr(xq), _ptr(s), t, k, n_out, _ptr(out), _stream_ptr(stream))
     _check(st, "sbn_bitlinear_grad_w")
+    return out
+
+
+ACTS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}   # SBN_ACT_*
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _need_shape(t: Optional[torch.Tensor], dtype, shape, what: str):
+    """The checks of an optional tensor argument of a given shape."""
+    if t is None:
+        return
+    _need(t, dtype, what)
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _apart(z: Optional[torch.Tensor], *others: Optional[torch.Tensor]):
+    if z is not None and any(o is not None and o.data_ptr() == z.data_ptr() for o in others):
+        raise ValueError("out_z must not be another tensor of the call")
+
+
+def _need_packed(w, dev: torch.device):
+    for t, what in ((w.codes, "codes"), (w.meta, "meta"), (w.gamma, "gamma")):
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{what} of the packed weights must be contiguous on {dev}")
+
+
+def _act_buffers(x, rows: int, w, lead, bias, residual, out, out_z, stream):
+    """Checks of the epilogue's tensors; the output, allocated if not given."""
+    _need_packed(w, x.device)
+    _need_shape(bias, torch.float32, lead + (w.n_out,), "bias")
+    _need_shape(residual, torch.bfloat16, (rows, w.n_out), "residual")
+    _need_shape(out, torch.bfloat16, (rows, w.n_out), "out")
+    _need_shape(out_z, torch.bfloat16, (rows, w.n_out), "out_z")
+    _one_device(x, bias, residual, out, out_z)
+    _apart(out_z, out, residual)
+    if out is None:
+        with _alloc_on(x.device, stream):
+            out = torch.empty((rows, w.n_out), dtype=torch.bfloat16, device=x.device)
+    return out
+
+
+def _scratch(need: int, workspace, dev: torch.device, stream):
+    if workspace is None:
+        if need == 0:
+            return None
+        with _alloc_on(dev, stream):
+            return torch.empty((need,), dtype=torch.uint8, device=dev)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    return workspace
+
+
+def bitlinear_act(xq: torch.Tensor, s: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tensor] = None,
+                  act: str = "none", residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  out_z: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
+    """sbn_bitlinear_act: y = f(z) + residual with z = acc gamma s_t / 127 + bias.
+
+    act: "none", "relu", "relu2", "silu" or "gelu". bias: fp32 [N_out];
+    residual: bf16 [T, N_out], may be `out` itself. out_z, if given, receives z
+    in bf16 (the input of act_grad). workspace: as for bitlinear."""
+    _need(xq, torch.int8, "xq")
+    t, k = xq.shape
+    if k != w.k:
+        raise ValueError("K mismatch between activations and weights")
+    _need_shape(s, torch.float32, (t,), "s")
+    _one_device(xq, s)
+    code = _act(act)
+    out = _act_buffers(xq, t, w, (), bias, residual, out, out_z, stream)
+    ws = None
+    if workspace is not False:
+        ws = _scratch(bitlinear_workspace_bytes(t, k, w.n_out), workspace, xq.device, stream)
+    _run_on(xq.device, "sbn_bitlinear_act", stream, _ptr(xq), _ptr(s), t, k, w.n_out, w.n, w.m, _ptr(w.codes),
+            _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(ws),
+            0 if ws is None else ws.numel())
+    return out
+
+
+def bitlinear_x_act(x: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tensor] = None, act: str = "none",
+                    residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    out_z: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
+                    out_s: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """sbn_bitlinear_x_act: bitlinear_act from bf16 activations (one kernel for
+    T <= 16). out_q / out_s, if given, receive Xq and s."""
+    _need(x, torch.bfloat16, "x")
+    t, k = x.shape
+    if k != w.k:
+        raise ValueError("K mismatch between activations and weights")
+    code = _act(act)
+    _need_shape(out_q, torch.int8, (t, k), "out_q")
+    _need_shape(out_s, torch.float32, (t,), "out_s")
+    _one_device(x, out_q, out_s)
+    out = _act_buffers(x, t, w, (), bias, residual, out, out_z, stream)
+    ws = _scratch(bitlinear_x_workspace_bytes(t, k, w.n_out), workspace, x.device, stream)
+    _run_on(x.device, "sbn_bitlinear_x_act", stream, _ptr(x), t, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta),
+            _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s),
+            _ptr(ws), ws.numel())
+    return out
+
+
+def act_grad(dy: torch.Tensor, z: torch.Tensor, act: str, offsets: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, out_bias: Optional[torch.Tensor] = None, stream=None):
+    """sbn_act_grad: (dz, dbias) of the epilogue, dz = dy f'(z) in bf16 and dbias
+    its column sums in fp32: [N_out], or [E, N_out] for rows grouped by the
+    int32 offsets [E + 1]. out may be dy itself; out_bias=False leaves the
+    sums out (dbias is None). The residual's gradient is dy."""
+    _need(dy, torch.bfloat16, "dy")
+    rows, n_out = dy.shape
+    _need_shape(z, torch.bfloat16, (rows, n_out), "z")
+    _need_shape(out, torch.bfloat16, (rows, n_out), "out")
+    code = _act(act)
+    experts, lead = 1, ()
+    if offsets is not None:
+        experts = _experts_of(offsets)
+        lead = (experts,)
+    with _alloc_on(dy.device, stream):
+        if out is None:
+            out = torch.empty_like(dy)
+        if out_bias is None:
+            out_bias = torch.empty(lead + (n_out,), dtype=torch.float32, device=dy.device)
+    dbias = None if out_bias is False else out_bias
+    _need_shape(dbias, torch.float32, lead + (n_out,), "out_bias")
+    _one_device(dy, z, offsets, out, dbias)
+    if out.data_ptr() == z.data_ptr():
+        raise ValueError("out must not be z")
+    _run_on(dy.device, "sbn_act_grad", stream, _ptr(dy), _ptr(z), rows, _ptr(offsets), experts, n_out, code, _ptr(out),
+            _ptr(dbias))
+    return out, dbias
+
+
+@dataclass
+class PackedExperts:
+    """Packed ternary weights of a set of layers of one shape, stacked."""
+    codes: torch.Tensor            # uint8 [E, n_out, codes_row_bytes]
+    meta: Optional[torch.Tensor]   # uint8 [E, n_out, meta_row_bytes] or None (n == m)
+    gamma: torch.Tensor            # float32 [E]
+    n_out: int
+    k: int
+    n: int
+    m: int
+    experts: int
+
+    def expert(self, e: int) -> PackedWeights:
+        """The packed weights of one expert (views)."""
+        return PackedWeights(self.codes[e], None if self.meta is None else self.meta[e], self.gamma[e:e + 1],
+                             self.n_out, self.k, self.n, self.m)
+
+
+def alloc_experts(experts: int, n_out: int, k: int, n: int, m: int, device) -> PackedExperts:
+    cr, mr = codes_row_bytes(k, n, m), meta_row_bytes(k, n, m)
+    if cr == 0:
+        raise SbnError(3, "alloc_experts")
+    codes = torch.empty((experts, n_out, cr), dtype=torch.uint8, device=device)
+    meta = torch.empty((experts, n_out, mr), dtype=torch.uint8, device=device) if mr else None
+    gamma = torch.empty((experts,), dtype=torch.float32, device=device)
+    return PackedExperts(codes, meta, gamma, n_out, k, n, m, experts)
+
+
+def quantize_experts(w: torch.Tensor, n: int, m: int, out: Optional[PackedExperts] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> PackedExperts:
+    """quantize_weights of every expert of w [E, N_out, K], each with its own gamma."""
+    _need(w, torch.bfloat16, "w")
+    experts, n_out, k = w.shape
+    with _alloc_on(w.device, stream):
+        if out is None:
+            out = alloc_experts(experts, n_out, k, n, m, w.device)
+        if workspace is None:
+            workspace = torch.empty(workspace_bytes(n_out, k), dtype=torch.uint8, device=w.device)
+    if (out.experts, out.n_out, out.k, out.n, out.m) != (experts, n_out, k, n, m):
+        raise ValueError("out describes other experts")
+    _one_device(w, out.codes, workspace)
+    for e in range(experts):
+        p = out.expert(e)
+        _run_on(w.device, "sbn_quantize_weights", stream, _ptr(w[e]), n_out, k, n, m, _ptr(p.codes), _ptr(p.meta),
+                _ptr(p.gamma), _ptr(workspace), workspace.numel())
+    return out
+
+
+def _experts_of(offsets: torch.Tensor) -> int:
+    _need(offsets, torch.int32, "offsets")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must have shape (experts + 1,)")
+    return offsets.numel() - 1
+
+
+def bitlinear_grouped(xq: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor, w: PackedExperts,
+                      bias: Optional[torch.Tensor] = None, act: str = "none",
+                      residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      out_z: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """sbn_bitlinear_grouped: bitlinear_act of every expert on its rows, rows
+    sorted by expert, expert e owning rows offsets[e] .. offsets[e + 1] - 1
+    (int32 [E + 1] on the device). bias: fp32 [E, N_out]. Rows outside
+    [offsets[0], offsets[E]) of `out` keep their values."""
+    _need(xq, torch.int8, "xq")
+    rows, k = xq.shape
+    if k != w.k:
+        raise ValueError("K mismatch between activations and weights")
+    if _experts_of(offsets) != w.experts:
+        raise ValueError("offsets and weights differ in experts")
+    _need_shape(s, torch.float32, (rows,), "s")
+    _one_device(xq, s, offsets)
+    code = _act(act)
+    out = _act_buffers(xq, rows, w, (w.experts,), bias, residual, out, out_z, stream)
+    _run_on(xq.device, "sbn_bitlinear_grouped", stream, _ptr(xq), _ptr(s), rows, _ptr(offsets), w.experts, k, w.n_out,
+            w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z),
+            _ptr(out))
+    return out
+
+
+def bitlinear_grouped_x(x: torch.Tensor, offsets: torch.Tensor, w: PackedExperts,
+                        bias: Optional[torch.Tensor] = None, act: str = "none",
+                        residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        out_z: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
+                        out_s: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """sbn_bitlinear_grouped_x: bitlinear_grouped from bf16 activations (one
+    kernel for up to 16 rows). out_q / out_s, if given, receive Xq and s of
+    every row."""
+    _need(x, torch.bfloat16, "x")
+    rows, k = x.shape
+    if k != w.k:
+        raise ValueError("K mismatch between activations and weights")
+    if _experts_of(offsets) != w.experts:
+        raise ValueError("offsets and weights differ in experts")
+    _need_shape(out_q, torch.int8, (rows, k), "out_q")
+    _need_shape(out_s, torch.float32, (rows,), "out_s")
+    _one_device(x, offsets, out_q, out_s)
+    code = _act(act)
+    out = _act_buffers(x, rows, w, (w.experts,), bias, residual, out, out_z, stream)
+    ws = _scratch(int(lib().sbn_bitlinear_grouped_x_workspace_bytes(rows, k)), workspace, x.device, stream)
+    _run_on(x.device, "sbn_bitlinear_grouped_x", stream, _ptr(x), rows, _ptr(offsets), w.experts, k, w.n_out, w.n, w.m,
+            _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out),
+            _ptr(out_q), _ptr(out_s), _ptr(ws), ws.numel())
+    return out
+
+
+def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedExperts,
+                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """sbn_bitlinear_grouped_grad_x: dX of every expert's rows (bf16 [R, K])."""
+    _need(dy, torch.bfloat16, "dy")
+    rows, n_out = dy.shape
+    if n_out != w.n_out:
+        raise ValueError("N_out mismatch between dY and the weights")
+    if _experts_of(offsets) != w.experts:
+        raise ValueError("offsets and weights differ in experts")
+    _need_shape(out, torch.bfloat16, (rows, w.k), "out")
+    _need_packed(w, dy.device)
+    _one_device(dy, offsets, out)
+    if out is None:
+        with _alloc_on(dy.device, stream):
+            out = torch.empty((rows, w.k), dtype=torch.bfloat16, device=dy.device)
+    _run_on(dy.device, "sbn_bitlinear_grouped_grad_x", stream, _ptr(dy), rows, _ptr(offsets), w.experts, w.k, n_out,
+            w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(out))
+    return out
+
+
+def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor,
+                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """sbn_bitlinear_grouped_grad_w: dW of every expert (bf16 [E, N_out, K])."""
+    _need(dy, torch.bfloat16, "dy")
+    _need(xq, torch.int8, "xq")
+    rows, n_out = dy.shape
+    if xq.shape[0] != rows:
+        raise ValueError("row mismatch between dY and Xq")
+    k = xq.shape[1]
+    experts = _experts_of(offsets)
+    _need_shape(s, torch.float32, (rows,), "s")
+    _need_shape(out, torch.bfloat16, (experts, n_out, k), "out")
+    _one_device(dy, xq, s, offsets, out)
+    if out is None:
+        with _alloc_on(dy.device, stream):
+            out = torch.empty((experts, n_out, k), dtype=torch.bfloat16, device=dy.device)
+    _run_on(dy.device, "sbn_bitlinear_grouped_grad_w", stream, _ptr(dy), _ptr(xq), _ptr(s), rows, _ptr(offsets),
+            experts, k, n_out, _ptr(out))
     return out
 
 
