@@ -2,13 +2,15 @@
 // column sums of dz (per expert where the rows are grouped).
 //
 // Bound by DRAM: dy and z are read and dz is written once, 6 bytes per
-// element. A cluster of eight CTAs owns 128 columns of one expert's rows: 16
-// lanes of eight columns (16-byte accesses) by 16 row lanes per CTA, so 128
-// rows are in work at a time. The column sums stay in registers (fp32, of
-// the unrounded dz), then go through shared memory and the cluster's
-// distributed shared memory in a fixed order: no workspace, no atomics, the
-// same sums every time. Where N_out is not a multiple of 8 a lane takes
-// every 16th column with 2-byte accesses.
+// element. A cluster of CTAs owns 64 columns of one expert's rows: 8 lanes of
+// eight columns (16-byte accesses, a 128-byte line per row) by 32 row lanes
+// per CTA. The column sums stay in registers (fp32, of the unrounded dz), then
+// go through shared memory and the cluster's distributed shared memory in a
+// fixed order: no workspace, no atomics, the same sums every time. The
+// cluster is as small (1, 2, 4 or 8 CTAs) as fills the GPU: the CTAs of a
+// cluster start and end together, and with eight of them per block of columns a
+// batch over 16 experts ran at a third of the bandwidth. Where N_out is not a
+// multiple of 8 a lane takes every 8th column with 2-byte accesses.
 #pragma once
 
 #include "common.cuh"
@@ -19,9 +21,9 @@
 namespace sbn {
 
 constexpr int kAgThreads = 256;
-constexpr int kAgCols = 128;       // columns per cluster
-constexpr int kAgCluster = 8;
-constexpr int kAgLanes = 16;       // row lanes per CTA
+constexpr int kAgCols = 64;        // columns per cluster
+constexpr int kAgColLanes = 8;
+constexpr int kAgLanes = kAgThreads / kAgColLanes;   // row lanes per CTA
 constexpr int kAgUnroll = 4;       // rows of a lane in flight
 
 struct AgParams {
@@ -32,17 +34,19 @@ struct AgParams {
   GrpParams grp;
   int N;
   int act;
+  int cluster;      // CTAs per cluster
 };
 
-// Grid (clusters of column blocks x 8, experts).
+// Grid (column blocks x cluster, experts).
 template <bool VEC>
 __global__ void __launch_bounds__(kAgThreads)
 act_grad_kernel(const AgParams p) {
   __shared__ float s_sum[kAgLanes][kAgCols];
   __shared__ float s_cta[kAgCols];
-  const int tid = threadIdx.x, lane_r = tid >> 4, lane_c = tid & 15;
-  const int rank = (int)cluster_rank();
-  const int c0 = (int)(blockIdx.x / kAgCluster) * kAgCols;
+  const int tid = threadIdx.x, lane_r = tid / kAgColLanes, lane_c = tid % kAgColLanes;
+  const int cs = p.cluster;
+  const int rank = (int)(blockIdx.x % (unsigned)cs);
+  const int c0 = (int)(blockIdx.x / (unsigned)cs) * kAgCols;
   const int e = (int)blockIdx.y;
   griddep_wait();
   int lo = 0, hi = p.grp.rows;
@@ -50,16 +54,16 @@ act_grad_kernel(const AgParams p) {
     lo = min(max(p.grp.offsets[e], 0), p.grp.rows);
     hi = min(max(p.grp.offsets[e + 1], 0), p.grp.rows);
   }
-  const int step = VEC ? 1 : kAgLanes;                       // distance between a lane's columns
+  const int step = VEC ? 1 : kAgColLanes;   // distance between a lane's columns
   const int col = c0 + (VEC ? 8 * lane_c : lane_c);
   float sum[8] = {};
-  for (int r0 = lo + rank * kAgLanes + lane_r; r0 < hi; r0 += kAgUnroll * kAgCluster * kAgLanes) {
+  for (int r0 = lo + rank * kAgLanes + lane_r; r0 < hi; r0 += kAgUnroll * cs * kAgLanes) {
     uint4 dv[kAgUnroll], zv[kAgUnroll];
     float d[8], z[8];
     if (VEC) {
 #pragma unroll
       for (int u = 0; u < kAgUnroll; ++u) {
-        const int r = r0 + u * kAgCluster * kAgLanes;
+        const int r = r0 + u * cs * kAgLanes;
         if (r < hi && col < p.N) {
           dv[u] = *reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col);
           zv[u] = *reinterpret_cast<const uint4*>(p.z + (size_t)r * p.N + col);
@@ -68,7 +72,7 @@ act_grad_kernel(const AgParams p) {
     }
 #pragma unroll
     for (int u = 0; u < kAgUnroll; ++u) {
-      const int r = r0 + u * kAgCluster * kAgLanes;
+      const int r = r0 + u * cs * kAgLanes;
       if (r >= hi || col >= p.N) continue;
       const size_t at = (size_t)r * p.N + col;
       if (VEC) {
@@ -115,12 +119,13 @@ act_grad_kernel(const AgParams p) {
 #pragma unroll
     for (int i = 0; i < kAgLanes; ++i) t += s_sum[i][tid];
     s_cta[tid] = t;
+    if (cs == 1 && c0 + tid < p.N) p.dbias[(size_t)e * p.N + c0 + tid] = t;
   }
+  if (cs == 1) return;
   cluster_sync_all();
   if (rank == 0 && tid < kAgCols && c0 + tid < p.N) {
     float t = 0.f;
-#pragma unroll
-    for (int c = 0; c < kAgCluster; ++c) {
+    for (int c = 0; c < cs; ++c) {
       float v;
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(smem_u32(&s_cta[tid]), (uint32_t)c)));
       t += v;

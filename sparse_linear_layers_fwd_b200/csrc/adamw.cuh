@@ -71,6 +71,13 @@ SBN_DEVFN uint32_t aw_mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// 1 / x within two steps of fp32 (only the parameters see it, not the states).
+SBN_DEVFN float aw_rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 2^e as a float, -126 <= e <= 127.
 SBN_DEVFN float aw_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -79,18 +86,26 @@ SBN_DEVFN float aw_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 2
 SBN_DEVFN int aw_scale_exp(uint32_t top_bits) { return max((int)(top_bits >> 23) - 127, -100); }
 
 // y >= 0 (below 2^8) to the e4m3 grid, whose step at y is
-// ulp = 2^(max(exponent, -6) - 3): with x = y / ulp and n = floor(x), to
-// n + 1 rather than n with probability x - n, or for SQUARE with the
-// probability (x^2 - n^2) / ((n + 1)^2 - n^2) that keeps the expected square.
+// ulp = 2^(max(exponent, -6) - 3): with lo the grid point at or below y, to
+// lo + ulp rather than lo with probability (y - lo) / ulp, or for SQUARE with
+// the probability (y^2 - lo^2) / ((lo + ulp)^2 - lo^2) that keeps the expected
+// square. u is uniform in [0, 1). Adding 2^23 ulp with rounding down drops the
+// bits below the step (conversions and floor would run on the special-function
+// unit at an eighth of the rate).
 template <bool SQUARE>
 SBN_DEVFN float aw_round(float y, float u) {
-  const uint32_t kf = max(__float_as_uint(y) >> 23, 121u);
-  const float inv = __uint_as_float((257u - kf) << 23), ulp = __uint_as_float((kf - 3u) << 23);
-  const float x = __fmul_rn(y, inv), n = floorf(x);
-  const float rem = __fsub_rn(x, n);
-  const bool up = SQUARE ? __fmul_rn(u, __fadd_rn(__fadd_rn(n, n), 1.f)) < __fmul_rn(rem, __fadd_rn(x, n)) : u < rem;
-  return __fmul_rn(up ? __fadd_rn(n, 1.f) : n, ulp);
+  const uint32_t k = max(__float_as_uint(y) & 0x7F800000u, 121u << 23);
+  const float ulp = __uint_as_float(k - (3u << 23)), big = __uint_as_float(k + (20u << 23));
+  const float lo = __fsub_rn(__fadd_rd(y, big), big);
+  const float rem = __fsub_rn(y, lo);
+  const float step = __fmul_rn(u, ulp);
+  const bool up = SQUARE ? __fmul_rn(step, __fadd_rn(__fadd_rn(lo, lo), ulp)) < __fmul_rn(rem, __fadd_rn(y, lo))
+                         : step < rem;
+  return up ? __fadd_rn(lo, ulp) : lo;
 }
+
+// 16 random bits as a float in [0, 1).
+SBN_DEVFN float aw_unit(uint32_t h16) { return __fsub_rn(__uint_as_float(0x3F800000u | (h16 << 7)), 1.f); }
 
 SBN_DEVFN void aw_decode2(uint16_t c, float& a, float& b) {
   uint32_t h;
@@ -190,7 +205,7 @@ SBN_DEVFN void aw_store_codes(uint8_t* p, float* scale, size_t i, int have, bool
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float y = __fmul_rn(fabsf(r[j]), up);
-    const float u = __fmul_rn((float)((h[j] >> (16 * half)) & 0xFFFFu), 1.f / 65536.f);
+    const float u = aw_unit(half ? h[j] >> 16 : h[j] & 0xFFFFu);
     float v = aw_round<ROOT>(y, u);
     if (ROOT && y > 0.f) v = fmaxf(v, 1.f / 512.f);
     q[j] = copysignf(v, r[j]);
@@ -255,7 +270,7 @@ adamw_kernel(const __grid_constant__ AwTable<N> tab, const AwHyper hp) {
       m[j] = __fadd_rn(__fmul_rn(hp.b1, m[j]), __fmul_rn(hp.omb1, gj));
       v[j] = __fadd_rn(__fmul_rn(hp.b2, v0), __fmul_rn(hp.omb2, __fmul_rn(gj, gj)));
       r[j] = __fsqrt_rn(v[j]);
-      const float u = __fdiv_rn(m[j], __fadd_rn(__fmul_rn(r[j], c2), hp.eps));
+      const float u = __fmul_rn(m[j], aw_rcp(__fadd_rn(__fmul_rn(r[j], c2), hp.eps)));
       p[j] = __fsub_rn(__fmul_rn(p[j], dec), __fmul_rn(a, u));
     }
     aw_store(pp, i, have, vec, p);

@@ -24,16 +24,46 @@ struct EpiParams {
   int act;
 };
 
-// Phi(z), the normal distribution function; erfc keeps its relative accuracy
-// for large negative z, where 1 + erf would cancel.
-SBN_DEVFN float epi_phi(float z) { return 0.5f * erfcf(-0.70710678f * z); }
+// 2^x and 1 / x on the special-function unit, each within two steps of fp32.
+SBN_DEVFN float epi_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+SBN_DEVFN float epi_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// exp(-z): the argument's rounding is |z| half steps, so the relative error
+// is about (|z| + 5) 2^-24. Infinity where it overflows, and 1 / (1 + exp(-z)) 0.
+SBN_DEVFN float epi_exp_neg(float z) { return epi_ex2(-1.44269504f * z); }
+SBN_DEVFN float epi_sigmoid(float z) { return epi_rcp(1.f + epi_exp_neg(z)); }
+
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2), which its
+// derivative needs too: the rational approximation 7.1.26 of Abramowitz and
+// Stegun's Handbook of Mathematical Functions for erfc(|z| / sqrt 2), within
+// 1.5e-7 absolute (half of it in Phi); a library erfc takes four times as
+// many instructions, which bound the kernels around it.
+SBN_DEVFN float epi_phi(float z, float& e) {
+  const float x = fabsf(z) * 0.70710678f;
+  e = epi_ex2(-0.72134752f * z * z);
+  const float t = epi_rcp(fmaf(0.3275911f, x, 1.f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q = 0.5f * q * t * e;
+  return z < 0.f ? q : 1.f - q;
+}
 
 SBN_DEVFN float act_f(int act, float z) {
   switch (act) {
     case kActRelu: return fmaxf(z, 0.f);
     case kActRelu2: { const float r = fmaxf(z, 0.f); return r * r; }
-    case kActSilu: return z / (1.f + expf(-z));
-    case kActGelu: return z * epi_phi(z);
+    case kActSilu: return z * epi_sigmoid(z);
+    case kActGelu: { float e; return z * epi_phi(z, e); }
     default: return z;
   }
 }
@@ -43,10 +73,14 @@ SBN_DEVFN float act_df(int act, float z) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
     case kActRelu2: return 2.f * fmaxf(z, 0.f);
     case kActSilu: {
-      const float s = 1.f / (1.f + expf(-z));
+      const float s = epi_sigmoid(z);
       return s * (1.f + z * (1.f - s));
     }
-    case kActGelu: return epi_phi(z) + z * expf(-0.5f * z * z) * 0.39894228f;
+    case kActGelu: {
+      float e;
+      const float phi = epi_phi(z, e);
+      return fmaf(z * 0.39894228f, e, phi);
+    }
     default: return 1.f;
   }
 }

@@ -234,10 +234,16 @@ sbn_status sbn_act_grad(const void* dy_bf16, const void* z_bf16, int32_t rows, c
   p.dy = reinterpret_cast<const uint16_t*>(dy_bf16); p.z = reinterpret_cast<const uint16_t*>(z_bf16);
   p.dz = reinterpret_cast<uint16_t*>(dz_bf16); p.dbias = dbias;
   p.grp = GrpParams{offsets, experts, rows}; p.N = n_out; p.act = act;
-  const dim3 grid((unsigned)((n_out + kAgCols - 1) / kAgCols * kAgCluster), (unsigned)experts);
+  // clusters along the rows until there are four CTAs per SM, while each has
+  // a row for each of its row lanes
+  const long long blocks = (long long)((n_out + kAgCols - 1) / kAgCols) * experts;
+  p.cluster = 1;
+  while (p.cluster < 8 && blocks * p.cluster < 4ll * sms && (long long)rows > (long long)p.cluster * kAgLanes * experts)
+    p.cluster *= 2;
+  const dim3 grid((unsigned)((n_out + kAgCols - 1) / kAgCols * p.cluster), (unsigned)experts);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return n_out % 8 == 0 ? launch_ex(act_grad_kernel<true>, grid, dim3(kAgThreads), 0, cs, kAgCluster, p)
-                        : launch_ex(act_grad_kernel<false>, grid, dim3(kAgThreads), 0, cs, kAgCluster, p);
+  return n_out % 8 == 0 ? launch_ex(act_grad_kernel<true>, grid, dim3(kAgThreads), 0, cs, (unsigned)p.cluster, p)
+                        : launch_ex(act_grad_kernel<false>, grid, dim3(kAgThreads), 0, cs, (unsigned)p.cluster, p);
 }
 
 sbn_status sbn_bitlinear_grouped(const int8_t* xq, const float* x_scale, int32_t rows, const int32_t* offsets,

@@ -11,13 +11,13 @@ fallback: if ``libsbn.so`` is missing, loading it raises.
 
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
-import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -129,7 +129,8 @@ def _check(status: int, where: str):
 
 def _stream_ptr(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: building a Stream object takes several microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -162,12 +163,20 @@ def _one_device(*tensors) -> torch.device:
 def _run_on(dev: torch.device, name: str, stream, *args):
     """Call entry point `name` with the stream appended, on the device of its
     tensors (made current for the call when another one is)."""
-    fn = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream_ptr(stream)), name)
-    else:
+    st = _status_on(dev, name, stream, *args)
+    if st != 0:
+        raise SbnError(st, name)
+
+
+def _status_on(dev: torch.device, name: str, stream, *args) -> int:
+    fn = getattr(_lib or lib(), name)
+    current = torch.cuda.current_device()
+    if dev.index != current:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream_ptr(stream)), name)
+            return fn(*args, _stream_ptr(stream))
+    if stream is None:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(current))
+    return fn(*args, _stream_ptr(stream))
 
 
 def _alloc_on(dev: torch.device, stream):
@@ -509,9 +518,11 @@ def _apart(z: Optional[torch.Tensor], *others: Optional[torch.Tensor]):
 
 
 def _need_packed(w, dev: torch.device):
-    for t, what in ((w.codes, "codes"), (w.meta, "meta"), (w.gamma, "gamma")):
-        if t is not None and (t.device != dev or not t.is_contiguous()):
-            raise ValueError(f"{what} of the packed weights must be contiguous on {dev}")
+    c, m, g = w.codes, w.meta, w.gamma
+    if c.device != dev or g.device != dev or (m is not None and m.device != dev):
+        raise ValueError(f"the packed weights must be on {dev}")
+    if not (c.is_contiguous() and g.is_contiguous() and (m is None or m.is_contiguous())):
+        raise ValueError("the packed weights must be contiguous")
 
 
 def _act_buffers(x, rows: int, w, lead, bias, residual, out, out_z, stream):
@@ -523,22 +534,38 @@ def _act_buffers(x, rows: int, w, lead, bias, residual, out, out_z, stream):
     _need_shape(out_z, torch.bfloat16, (rows, w.n_out), "out_z")
     _one_device(x, bias, residual, out, out_z)
     _apart(out_z, out, residual)
-    if out is None:
-        with _alloc_on(x.device, stream):
-            out = torch.empty((rows, w.n_out), dtype=torch.bfloat16, device=x.device)
-    return out
+    return _new((rows, w.n_out), torch.bfloat16, x.device, stream) if out is None else out
+
+
+def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """An uninitialized tensor that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with _alloc_on(dev, stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _scratch(need: int, workspace, dev: torch.device, stream):
     if workspace is None:
-        if need == 0:
-            return None
-        with _alloc_on(dev, stream):
-            return torch.empty((need,), dtype=torch.uint8, device=dev)
+        return _new((need,), torch.uint8, dev, stream) if need else None
     _need(workspace, torch.uint8, "workspace")
     if workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}")
     return workspace
+
+
+def _run_with_scratch(dev: torch.device, name: str, stream, try_without: bool, workspace, need, args) -> None:
+    """A call whose workspace is last among its arguments. A decode call mostly
+    needs none: it is tried without one first (the library refuses it before
+    anything is enqueued) when the caller gave none."""
+    if workspace is None and try_without:
+        st = _status_on(dev, name, stream, *args, None, 0)
+        if st == 0:
+            return
+        if SBN_STATUS[st] != "SBN_ERR_WORKSPACE":
+            raise SbnError(st, name)
+    ws = _scratch(need(), workspace, dev, stream)
+    _run_on(dev, name, stream, *args, _ptr(ws), ws.numel())
 
 
 def bitlinear_act(xq: torch.Tensor, s: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tensor] = None,
@@ -582,10 +609,10 @@ def bitlinear_x_act(x: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tens
     _need_shape(out_s, torch.float32, (t,), "out_s")
     _one_device(x, out_q, out_s)
     out = _act_buffers(x, t, w, (), bias, residual, out, out_z, stream)
-    ws = _scratch(bitlinear_x_workspace_bytes(t, k, w.n_out), workspace, x.device, stream)
-    _run_on(x.device, "sbn_bitlinear_x_act", stream, _ptr(x), t, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta),
-            _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s),
-            _ptr(ws), ws.numel())
+    args = (_ptr(x), t, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code,
+            _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s))
+    _run_with_scratch(x.device, "sbn_bitlinear_x_act", stream, t <= 16, workspace,
+                      lambda: bitlinear_x_workspace_bytes(t, k, w.n_out), args)
     return out
 
 
@@ -604,11 +631,10 @@ def act_grad(dy: torch.Tensor, z: torch.Tensor, act: str, offsets: Optional[torc
     if offsets is not None:
         experts = _experts_of(offsets)
         lead = (experts,)
-    with _alloc_on(dy.device, stream):
-        if out is None:
-            out = torch.empty_like(dy)
-        if out_bias is None:
-            out_bias = torch.empty(lead + (n_out,), dtype=torch.float32, device=dy.device)
+    if out is None:
+        out = _new((rows, n_out), torch.bfloat16, dy.device, stream)
+    if out_bias is None:
+        out_bias = _new(lead + (n_out,), torch.float32, dy.device, stream)
     dbias = None if out_bias is False else out_bias
     _need_shape(dbias, torch.float32, lead + (n_out,), "out_bias")
     _one_device(dy, z, offsets, out, dbias)
@@ -718,10 +744,10 @@ def bitlinear_grouped_x(x: torch.Tensor, offsets: torch.Tensor, w: PackedExperts
     _one_device(x, offsets, out_q, out_s)
     code = _act(act)
     out = _act_buffers(x, rows, w, (w.experts,), bias, residual, out, out_z, stream)
-    ws = _scratch(int(lib().sbn_bitlinear_grouped_x_workspace_bytes(rows, k)), workspace, x.device, stream)
-    _run_on(x.device, "sbn_bitlinear_grouped_x", stream, _ptr(x), rows, _ptr(offsets), w.experts, k, w.n_out, w.n, w.m,
-            _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out),
-            _ptr(out_q), _ptr(out_s), _ptr(ws), ws.numel())
+    args = (_ptr(x), rows, _ptr(offsets), w.experts, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta),
+            _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s))
+    _run_with_scratch(x.device, "sbn_bitlinear_grouped_x", stream, rows <= 16, workspace,
+                      lambda: int(lib().sbn_bitlinear_grouped_x_workspace_bytes(rows, k)), args)
     return out
 
 
@@ -738,8 +764,7 @@ def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedE
     _need_packed(w, dy.device)
     _one_device(dy, offsets, out)
     if out is None:
-        with _alloc_on(dy.device, stream):
-            out = torch.empty((rows, w.k), dtype=torch.bfloat16, device=dy.device)
+        out = _new((rows, w.k), torch.bfloat16, dy.device, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_x", stream, _ptr(dy), rows, _ptr(offsets), w.experts, w.k, n_out,
             w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(out))
     return out
@@ -759,8 +784,7 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
     _need_shape(out, torch.bfloat16, (experts, n_out, k), "out")
     _one_device(dy, xq, s, offsets, out)
     if out is None:
-        with _alloc_on(dy.device, stream):
-            out = torch.empty((experts, n_out, k), dtype=torch.bfloat16, device=dy.device)
+        out = _new((experts, n_out, k), torch.bfloat16, dy.device, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_w", stream, _ptr(dy), _ptr(xq), _ptr(s), rows, _ptr(offsets),
             experts, k, n_out, _ptr(out))
     return out
@@ -828,9 +852,6 @@ class AdamW:
             self.m_scales = [torch.ones(b, dtype=torch.float32, **kw) for b in blocks]
             self.v_scales = [torch.ones(b, dtype=torch.float32, **kw) for b in blocks]
         self.step_state = torch.zeros(2, dtype=torch.int32, **kw)
-        # entries of sbn_adamw_tensor, eight 64-bit words each; the gradient
-        # pointers are filled in by step()
-        self._table = np.zeros((len(self.params), 8), dtype=np.int64)
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
         """One step with the gradients of params (same order and sizes, all
@@ -841,12 +862,16 @@ class AdamW:
         gd = grads[0].dtype
         if gd not in (torch.float32, torch.bfloat16):
             raise TypeError(f"grads must be float32 or bfloat16, got {gd}")
-        for g, p in zip(grads, self.params):
-            if g.dtype != gd or g.device != self.device or not g.is_contiguous() or g.numel() != p.numel():
+        sizes = [p.numel() for p in self.params]
+        for g, n in zip(grads, sizes):
+            if g.dtype is not gd or g.device != self.device or not g.is_contiguous() or g.numel() != n:
                 _need(g, gd, "grads")
                 raise ValueError("a gradient differs from its parameter in size or device")
-            if p.device != self.device or not p.is_contiguous():
-                raise ValueError("a parameter has been moved since the optimizer was made")
+        if [p.device for p in self.params] != [self.device] * len(sizes) or not all(p.is_contiguous() for p in self.params):
+            raise ValueError("a parameter has been moved since the optimizer was made")
+        for ts in (self.m, self.v):
+            if [t.numel() for t in ts] != sizes:
+                raise ValueError("a state tensor differs from its parameter in size")
         lr_dev = None
         lr = self.lr
         for t, what in ((lr if isinstance(lr, torch.Tensor) else None, "lr"), (grad_scale, "grad_scale")):
@@ -857,18 +882,15 @@ class AdamW:
                 _one_device(self.params[0], t)
         if isinstance(lr, torch.Tensor):
             lr_dev, lr = lr, 0.0
-        tab = self._table
-        tab[:, 0] = [p.data_ptr() for p in self.params]
-        tab[:, 1] = [g.data_ptr() for g in grads]
-        tab[:, 2] = [t.data_ptr() for t in self.m]
-        tab[:, 3] = [t.data_ptr() for t in self.v]
-        if self.state_bits == 8:
-            tab[:, 4] = [t.data_ptr() for t in self.m_scales]
-            tab[:, 5] = [t.data_ptr() for t in self.v_scales]
-        if self.copies is not None:
-            tab[:, 6] = [t.data_ptr() for t in self.copies]
-        tab[:, 7] = [p.numel() for p in self.params]
-        _run_on(self.device, "sbn_adamw", stream, tab.ctypes.data, len(self.params),
+        none = [0] * len(self.params)
+        eight = self.state_bits == 8
+        ptr = torch.Tensor.data_ptr
+        # entries of sbn_adamw_tensor: eight 64-bit words each
+        words = [x for e in zip(map(ptr, self.params), map(ptr, grads), map(ptr, self.m), map(ptr, self.v),
+                                map(ptr, self.m_scales) if eight else none, map(ptr, self.v_scales) if eight else none,
+                                none if self.copies is None else map(ptr, self.copies), sizes) for x in e]
+        table = array.array("q", words)
+        _run_on(self.device, "sbn_adamw", stream, table.buffer_info()[0], len(self.params),
                 int(self.params[0].dtype == torch.bfloat16), int(gd == torch.bfloat16), self.state_bits,
                 _ptr(self.step_state), float(lr), _ptr(lr_dev), float(self.betas[0]), float(self.betas[1]),
                 float(self.eps), float(self.weight_decay), _ptr(grad_scale), int(self.seed) & 0xFFFFFFFF)

@@ -6,8 +6,8 @@ Tolerances of the fp32 step, u = 2^-24 (half a step of fp32): b1 m and
 so m is within 3 u of M = |b1 m| + |(1 - b1) g|; v likewise within 4 u
 (one product more). 6 u and 8 u are asserted. The update a m / (r c2 + eps)
 has a: lr / bc1 (expm1f is within 2 steps = 4 u, argument 1 u, division 1 u:
-6 u), the root of v (2 + 1 u), c2 (4 u), product and sum (2 u), quotient and
-product (2 u): 17 u of a M / den in all with m's own 6 u on top; 32 u is
+6 u), the root of v (2 + 1 u), c2 (4 u), product and sum (2 u), reciprocal (4 u) and
+two products (2 u): 21 u of a M / den in all with m's own 6 u on top; 32 u is
 asserted, plus 3 u |p| for the decay's coefficient, product and the last
 difference.
 """

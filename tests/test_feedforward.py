@@ -7,11 +7,16 @@ Tolerances, u = 2^-24 (half a step of fp32), h = 2^-8 (of bf16):
   z   acc (exact below 2^24, else 1 u) times a factor of three roundings, one
       product, one sum: within 6 u of Z = |acc gamma s / 127| + |bias|;
   f   relu2 doubles a relative error (its slope is 2 |z|); the slopes of the
-      others are below 1.13; their own evaluation (expf, erfcf: a few steps,
-      a division, products) stays below 16 u of |f|, for silu's and gelu's
-      exponents up to |z| = 30: expf's argument is exact here;
+      others are below 1.13. Their own evaluation: relu2 one product; silu an
+      exponential whose argument -z log2 e carries two roundings (2 |z| u of the
+      result, by d 2^x = 2^x ln 2 dx) and 4 u of its own, a sum, a reciprocal of
+      4 u, a product: (2 |z| + 12) u |f|; gelu the rational approximation of
+      Abramowitz and Stegun 7.1.26, 1.5e-7 of erfc and so 0.75e-7 of Phi, with
+      at most 2^-23 more of the fp32 evaluation (Phi <= 1, five products and
+      sums of terms below 2, two special functions; the exponential's argument
+      error z^2 u of a result below exp(-z^2 / 2) stays below u): 2e-7 |z|;
   y   one sum and one rounding to bf16:
-      h |y| + (1 + h) (6 u slope Z + 16 u |f| + u |y|).
+      h |y| + (1 + h) (6 u slope Z + error of f + u |y|).
   dX, dW  sums of n products exact in fp32 (dW: within 2^-17 of a, two bf16
       parts and the product with s / 127), accumulated in fp32 in any order:
       n u times the sum of |products|, doubled for the tensor core's
@@ -215,7 +220,8 @@ def reference(layer, q, s, spans, bias, act, residual):
     f = f64(act, z)
     slope = 2 * z.abs() + 1 if act == "relu2" else 1.13
     y = f if residual is None else f + residual.double()
-    err = 6 * U * slope * mag + 16 * U * f.abs() + U * y.abs()
+    own = {"silu": (2 * z.abs() + 12) * U * f.abs(), "gelu": 2e-7 * z.abs()}.get(act, 2 * U * f.abs())
+    err = 6 * U * slope * mag + own + U * y.abs()
     return y, H * y.abs() + (1 + H) * err, z, H * z.abs() + (1 + H) * 6 * U * mag
 
 
@@ -433,9 +439,11 @@ def test_offsets_out_of_order_stay_in_bounds(sbn_lib, cuda_ok, rows, experts):
 @pytest.mark.parametrize("rows,n_out,sizes", [(1, 1, None), (37, 264, None), (300, 129, (0, 250, 0, 50)),
                                               (1500, 200, (1000, 1, 499)), (70, 4864, (64, 0, 3))])
 def test_act_grad(sbn_lib, cuda_ok, act, rows, n_out, sizes):
-    """dz within one bf16 rounding and the derivative's evaluation (16 u of
-    |dy|(|f'| + 1): gelu's two terms may cancel), dbias within the fp32 sum's
-    n u of the sum of |dz| terms plus that; the same bits on every run."""
+    """dz within one bf16 rounding and the derivative's evaluation: silu's
+    s (1 + z (1 - s)) has s within (2 |z| + 9) u of itself, so the bracket is
+    within (|z| + 1) (2 |z| + 12) u; gelu's Phi is within 2e-7 and z phi within
+    (z^2 + 8) u |z phi| < 8 u; times |dy|. dbias within the fp32 sum's n u of the
+    sum of |dz| plus the terms' own errors; the same bits on every run."""
     from test_canaries import Guarded
     sbn = _sbn()
     g = torch.Generator(device="cuda").manual_seed(rows)
@@ -456,7 +464,9 @@ def test_act_grad(sbn_lib, cuda_ok, act, rows, n_out, sizes):
     sbn.act_grad(dy, z, act, offsets=o, out=dz, out_bias=db)
     gd.check()
     ref = dy.double() * df64(act, z.double())
-    e = 16 * U * dy.double().abs() * (df64(act, z.double()).abs() + 1)
+    az = z.double().abs()
+    own = {"silu": (az + 2) * (2 * az + 12) * U, "gelu": 2e-7 + 8 * U + 0 * az}.get(act, 2 * U * (2 * az + 1))
+    e = dy.double().abs() * own
     close(dz[inside], ref[inside], (H * ref.abs() + (1 + H) * e)[inside], "dz")
     assert (dz[~inside] == 5.0).all()
     for i, (a, b) in enumerate(spans):
