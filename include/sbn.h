@@ -565,7 +565,7 @@ sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq,
  *   lr, lr_dev    the learning rate, from the device word lr_dev if not NULL.
  *   grad_scale    optional device word: the gradients are multiplied by it first.
  * Errors: SBN_ERR_NULL, SBN_ERR_SHAPE (count, numel, state_bits, betas
- * outside [0, 1), eps below 0, a copy of bf16 parameters), SBN_ERR_ALIGN
+ * outside [0, 1), eps below FLT_MIN, a copy of bf16 parameters), SBN_ERR_ALIGN
  * (before anything is enqueued); SBN_ERR_CUDA.
  */
 typedef struct {

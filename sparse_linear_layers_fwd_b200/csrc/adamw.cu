@@ -4,6 +4,7 @@
 #include "sbn.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -84,7 +85,7 @@ extern "C" sbn_status sbn_adamw(const sbn_adamw_tensor* tensors, int32_t count, 
                                 void* stream) {
   if (!tensors || !step) return SBN_ERR_NULL;
   if (count < 1 || (state_bits != 8 && state_bits != 32)) return SBN_ERR_SHAPE;
-  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= FLT_MIN) || !std::isfinite(eps) ||
       !std::isfinite(lr) || !std::isfinite(weight_decay))
     return SBN_ERR_SHAPE;
   if (off_by(step, 4) || off_by(lr_dev, 4) || off_by(grad_scale, 4)) return SBN_ERR_ALIGN;

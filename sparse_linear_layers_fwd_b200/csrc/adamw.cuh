@@ -71,10 +71,10 @@ SBN_DEVFN uint32_t aw_mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// 1 / x within two steps of fp32 (only the parameters see it, not the states).
+// 1 / x within two steps of fp32, x >= FLT_MIN (only the parameters see it, not the states).
 SBN_DEVFN float aw_rcp(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -85,27 +85,37 @@ SBN_DEVFN float aw_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 2
 // codes of the block then lie below 2^8 (e4m3 reaches 448).
 SBN_DEVFN int aw_scale_exp(uint32_t top_bits) { return max((int)(top_bits >> 23) - 127, -100); }
 
-// y >= 0 (below 2^8) to the e4m3 grid, whose step at y is
-// ulp = 2^(max(exponent, -6) - 3): with lo the grid point at or below y, to
-// lo + ulp rather than lo with probability (y - lo) / ulp, or for SQUARE with
-// the probability (y^2 - lo^2) / ((lo + ulp)^2 - lo^2) that keeps the expected
-// square. u is uniform in [0, 1). Adding 2^23 ulp with rounding down drops the
-// bits below the step (conversions and floor would run on the special-function
-// unit at an eighth of the rate).
-template <bool SQUARE>
-SBN_DEVFN float aw_round(float y, float u) {
-  const uint32_t k = max(__float_as_uint(y) & 0x7F800000u, 121u << 23);
-  const float ulp = __uint_as_float(k - (3u << 23)), big = __uint_as_float(k + (20u << 23));
-  const float lo = __fsub_rn(__fadd_rd(y, big), big);
-  const float rem = __fsub_rn(y, lo);
-  const float step = __fmul_rn(u, ulp);
-  const bool up = SQUARE ? __fmul_rn(step, __fadd_rn(__fadd_rn(lo, lo), ulp)) < __fmul_rn(rem, __fadd_rn(y, lo))
-                         : step < rem;
-  return up ? __fadd_rn(lo, ulp) : lo;
+// The e4m3 grid at y >= 0 (below 2^8): three mantissa bits, a fixed step of
+// 2^-9 below 2^-6. Adding 2^-6 to such a y puts its steps where a normal
+// number has them, in the top three bits of the mantissa.
+constexpr uint32_t kAwGridMask = 0xFFF00000u;
+SBN_DEVFN float aw_grid_base(float y) { return y < 0.015625f ? 0.015625f : 0.f; }
+
+// y to the grid: up from the point at or below it with probability (distance)
+// / step, that is iff u < distance / step with u = h16 / 2^16 and the distance
+// the 20 mantissa bits below the grid. A carry out of them does the step: it
+// happens iff bits + (2^20 - 1 - 16 h16) >= 2^20, that is bits > 16 h16. The
+// base is added rounding up: bits beyond the sum's last, which u * step never
+// has, then still count as "above".
+SBN_DEVFN float aw_round(float y, uint32_t h16) {
+  const float base = aw_grid_base(y);
+  const uint32_t w = __float_as_uint(__fadd_ru(y, base));
+  return __fsub_rn(__uint_as_float((w + ((h16 << 4) ^ 0xFFFFFu)) & kAwGridMask), base);
 }
 
-// 16 random bits as a float in [0, 1).
-SBN_DEVFN float aw_unit(uint32_t h16) { return __fsub_rn(__uint_as_float(0x3F800000u | (h16 << 7)), 1.f); }
+// The same with the probability that keeps the expected square: between lo
+// and lo + ulp iff u ((lo + ulp)^2 - lo^2) < y^2 - lo^2. No y > 0 becomes 0.
+SBN_DEVFN float aw_round_root(float y, uint32_t h16) {
+  const float base = aw_grid_base(y);
+  const uint32_t w = __float_as_uint(__fadd_rz(y, base)) & kAwGridMask;
+  const float lo = __fsub_rn(__uint_as_float(w), base);
+  const float ulp = __uint_as_float((w & 0x7F800000u) - (3u << 23));
+  // 16 random bits as a float in [0, 1); conversions would run at an eighth of the rate
+  const float u = __fsub_rn(__uint_as_float(0x3F800000u | (h16 << 7)), 1.f);
+  const bool up = __fmul_rn(__fmul_rn(u, ulp), __fmaf_rn(2.f, lo, ulp)) < __fmul_rn(__fsub_rn(y, lo), __fadd_rn(y, lo));
+  const float q = up ? __fadd_rn(lo, ulp) : lo;
+  return y > 0.f ? fmaxf(q, 1.f / 512.f) : q;
+}
 
 SBN_DEVFN void aw_decode2(uint16_t c, float& a, float& b) {
   uint32_t h;
@@ -191,24 +201,20 @@ SBN_DEVFN void aw_load_codes(const uint8_t* p, size_t i, int have, bool vec, flo
 }
 
 // Codes of eight elements of a warp's block and the block's scale (lane 0).
-// ROOT: r = sqrt(v), whose square is kept in expectation. half: 0 takes the low, 1 the high 16 bits of the random words.
+// ROOT: r = sqrt(v), with the high half of the random words; else m, the low.
 template <bool ROOT>
 SBN_DEVFN void aw_store_codes(uint8_t* p, float* scale, size_t i, int have, bool vec, const float (&r)[8],
-                              const uint32_t (&h)[8], int half) {
-  uint32_t top = 0u;
+                              const uint32_t (&h)[8]) {
+  float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(r[j]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  const int e = aw_scale_exp(top);
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(r[j]));
+  const int e = aw_scale_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
   const float up = aw_pow2(7 - e);
   float q[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float y = __fmul_rn(fabsf(r[j]), up);
-    const float u = aw_unit(half ? h[j] >> 16 : h[j] & 0xFFFFu);
-    float v = aw_round<ROOT>(y, u);
-    if (ROOT && y > 0.f) v = fmaxf(v, 1.f / 512.f);
-    q[j] = copysignf(v, r[j]);
+    q[j] = ROOT ? aw_round_root(y, h[j] >> 16) : copysignf(aw_round(y, h[j] & 0xFFFFu), r[j]);
   }
   uint2 c;
   c.x = (uint32_t)aw_encode2(q[0], q[1]) | ((uint32_t)aw_encode2(q[2], q[3]) << 16);
@@ -282,12 +288,14 @@ adamw_kernel(const __grid_constant__ AwTable<N> tab, const AwHyper hp) {
       const uint32_t key = aw_mix(hp.seed + (uint32_t)t * kAwHashA + (tab.id0 + (uint32_t)lo) * kAwHashB);
       uint32_t h[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[j] = aw_mix(((uint32_t)i + (uint32_t)j) ^ key);
-        if (j >= have) m[j] = r[j] = 0.f;   // behind the tensor's end
+      for (int j = 0; j < 8; ++j) h[j] = aw_mix(((uint32_t)i + (uint32_t)j) ^ key);
+      if (have < 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= have) m[j] = r[j] = 0.f;   // behind the tensor's end
       }
-      aw_store_codes<false>(reinterpret_cast<uint8_t*>(e.m), e.ms + blk, i, have, vec, m, h, 0);
-      aw_store_codes<true>(reinterpret_cast<uint8_t*>(e.v), e.vs + blk, i, have, vec, r, h, 1);
+      aw_store_codes<false>(reinterpret_cast<uint8_t*>(e.m), e.ms + blk, i, have, vec, m, h);
+      aw_store_codes<true>(reinterpret_cast<uint8_t*>(e.v), e.vs + blk, i, have, vec, r, h);
     }
   }
   griddep_launch_dependents();

@@ -352,8 +352,8 @@ bl_gemv_grp_kernel(const GgParams p) {
       *ap = 0;
       if (o < p.N) {
         const size_t at = (size_t)row * p.N + o;
-        float z = __fmul_rn((float)av, __fdiv_rn(__fmul_rn(gm, s_scale[row]), 127.0f));
-        if (p.ep.bias) z = __fadd_rn(z, __ldg(p.ep.bias + (size_t)ex.z * p.N + o));
+        const float bias = p.ep.bias ? __ldg(p.ep.bias + (size_t)ex.z * p.N + o) : 0.f;
+        const float z = __fmaf_rn((float)av, __fdiv_rn(__fmul_rn(gm, s_scale[row]), 127.0f), bias);
         if (p.ep.z) p.ep.z[at] = f32_to_bf16_bits(z);
         float yv = act_f(p.ep.act, z);
         if (p.ep.residual) yv = __fadd_rn(yv, bf16_bits_to_float(p.ep.residual[at]));

@@ -90,7 +90,8 @@ struct T2Cfg {
   // K-major, N = BN, M = 256
   static constexpr uint32_t IDESC = (SPARSE ? (1u << 2) : 0u) | (2u << 4) | (1u << 7) | (1u << 10) |
                                     ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + YBUF + (2 * STAGES + 6) * 8 + 16;
+  static constexpr int SCBUF = (kT2Epi / 32) * 128;      // 32 token factors per epilogue warp
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + YBUF + SCBUF + (2 * STAGES + 6) * 8 + 16;
   static_assert(STAGE % 1024 == 0, "stages must stay 1024-byte aligned");
   static_assert(!SPARSE || ECOL + 8 * STAGES <= kT2TmemCols, "metadata ring must fit in TMEM");
   static_assert(SPARSE || 2 * BN <= (int)kT2TmemCols, "accumulators must fit in TMEM");
@@ -152,7 +153,8 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ybuf = smem + (size_t)C::STAGES * C::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ybuf + C::YBUF);
+  float* scbuf = reinterpret_cast<float*>(ybuf + C::YBUF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ybuf + C::YBUF + C::SCBUF);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;   // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2] this CTA's epilogue warps
@@ -321,7 +323,7 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
     constexpr int NCH = (kChunks + 1) / 2;
     const int nch = c_end - c_first;
     const float g = ACC ? 0.f : __ldg(p.gamma);
-    [[maybe_unused]] EpiTile et{wbuf, 0};
+    [[maybe_unused]] EpiTile et{wbuf, scbuf + 32 * (warp - 4), 0};
     [[maybe_unused]] const EpiOut eo{&tmap_y, &tmap_z, p.y, p.N, p.T, y_tma != 0};
     int jt = 0;
     for (int tile = pair; tile < n_tiles; tile += npairs, ++jt) {

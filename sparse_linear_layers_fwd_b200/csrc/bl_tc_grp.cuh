@@ -7,18 +7,28 @@
 // bias_e) + residual. Without offsets it is one layer over all rows.
 //
 // A persistent CTA per SM walks the tiles of the work list (grp.cuh): 128
-// output features x up to 256 rows of one expert, an expert's rows split into
-// equal tiles (a multiple of 16 rows each, the MMA's N). The weights are
-// expanded in shared memory by eight producer warps, since an expert sees few
-// rows: writing the expanded weights to memory and reading them back would
-// cost as much as the product itself at 500 rows.
-//   warp 0      TMA of the activation rows (boxes of 64 and 16 rows);
+// output features x up to 192 rows of one expert, an expert's rows split into
+// equal tiles (a multiple of 16 rows each, the MMA's N). The packed weights
+// are read once per tile and expanded on the way to the MMA, since an expert
+// sees few rows: expanding them in memory first would cost as much as the
+// product itself at 500 rows.
+//
+// The expanded weights go from the producers' registers straight into tensor
+// memory, as the MMA's A operand (lane = feature, 32-bit column = four
+// positions): they never touch shared memory, whose bandwidth the activations
+// need (read by the MMA at 64 bytes a cycle, written by TMA at the same rate).
+//   warp 0      TMA of the activation rows (boxes of 64 and 16 rows), stages of
+//               256 positions;
 //   warp 1      TMEM allocation and the MMA thread;
-//   warp 2      the work list;
-//   warps 4-11  producers (bl_tc.cuh), with the expansion of bl_gemv.cuh;
+//   warp 2      the work list, then TMA of the packed rows (codes and keep
+//               bits of 128 features x 256 positions) into a ring of their own;
+//   warps 4-11  producers: two groups of four warps take 128-position blocks
+//               in turn; a thread expands its feature's block (bl_gemv.cuh's
+//               expansion) into 32 registers, one tcgen05.st;
 //   warps 12-15 epilogue (epi_tile.cuh).
-// Rows of the next expert that share a box are loaded and multiplied, never
-// stored. All waits are bounded in time.
+// TMEM: two accumulators of 192 columns, four A slots of 32 columns. Rows of
+// the next expert that share a box are loaded and multiplied, never stored.
+// All waits are bounded in time.
 #pragma once
 
 #include <cuda.h>
@@ -33,17 +43,23 @@
 namespace sbn {
 
 constexpr int kTgBM = 128;
-constexpr int kTgBN = 256;
-constexpr int kTgStages = 4;
-constexpr int kTgABytes = kTgBM * 128;
-constexpr int kTgStageBytes = kTgABytes + kTgBN * 128;
+constexpr int kTgBN = 192;
+constexpr int kTgStages = 3;                   // activation stages of 256 positions
+constexpr int kTgSub = kTgBN * 128;            // one 128-position block of a stage
+constexpr int kTgStageBytes = 2 * kTgSub;
+constexpr int kTgSlots = 4;                    // A slots in TMEM
+constexpr uint32_t kTgACol = 2 * kTgBN;
+static_assert(kTgACol + 32 * kTgSlots <= kTcTmemCols, "accumulators and A slots fit in TMEM");
+constexpr int kTgPacked = 4;                   // packed stages of 256 positions
+constexpr int kTgPackedBytes = kTgBM * (64 + 32);
 constexpr int kTgSelCopies = 4;
-constexpr int kTgYBuf = (kTcEpilogue / 32) * 4096;
+constexpr int kTgYBuf = (kTcEpilogue / 32) * (4096 + 128);
+constexpr int kTgBars = 2 * (kTgStages + kTgSlots + kTgPacked) + 4;
 constexpr uint32_t kTgIdesc0 = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTgBM >> 4) << 24);
 
 __host__ __device__ inline size_t tg_smem_bytes(int experts) {
-  return 1024 + (size_t)kTgStages * kTgStageBytes + kTgYBuf + 256 * 8 * kTgSelCopies + (2 * kTgStages + 4) * 8 + 16 +
-         2 * 4 * (size_t)(experts + 1);
+  return 1024 + (size_t)kTgStages * kTgStageBytes + kTgPacked * kTgPackedBytes + kTgYBuf + 256 * 8 * kTgSelCopies +
+         kTgBars * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
 }
 
 struct TgParams {
@@ -81,17 +97,30 @@ SBN_DEVFN TgTile tg_tile(const int* off, const int* first, const GrpParams& g, i
   return t;
 }
 
-SBN_DEVFN void tc_mma_i8_n(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// A from tensor memory, B from shared memory.
+SBN_DEVFN void tc_mma_i8_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n}\n" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(0u)
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(0u)
       : "memory");
+}
+// 32 columns of this warp's 32 lanes from registers, and the wait for them.
+SBN_DEVFN void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
 // 64 positions (one span of bl_gemv.cuh) -> 16 words of int8.
 template <int MM, int CB, bool DENSE>
-SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* sel, uint32_t (&w)[16]) {
+SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* sel, uint32_t* w) {
   gv_expand<MM, CB, DENSE, 0, kTgSelCopies>(cw, mw, sel, w[0], w[1]);
   gv_expand<MM, CB, DENSE, 1, kTgSelCopies>(cw, mw, sel, w[2], w[3]);
   gv_expand<MM, CB, DENSE, 2, kTgSelCopies>(cw, mw, sel, w[4], w[5]);
@@ -105,34 +134,56 @@ SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], co
 template <int MM, int CB, bool DENSE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_constant__ CUtensorMap tmap_x16,
+                 const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_m,
                  const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_z,
                  const TgParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ybuf = smem + (size_t)kTgStages * kTgStageBytes;
+  uint8_t* packed = smem + (size_t)kTgStages * kTgStageBytes;
+  uint8_t* ybuf = packed + kTgPacked * kTgPackedBytes;
   uint2* s_sel = reinterpret_cast<uint2*>(ybuf + kTgYBuf);   // [256][kTgSelCopies]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
-  uint64_t* empty = full + kTgStages;
-  uint64_t* acc_full = empty + kTgStages;   // [2]
-  uint64_t* acc_empty = acc_full + 2;       // [2]
+  uint64_t* b_full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
+  uint64_t* b_empty = b_full + kTgStages;
+  uint64_t* a_full = b_empty + kTgStages;
+  uint64_t* a_empty = a_full + kTgSlots;
+  uint64_t* p_full = a_empty + kTgSlots;
+  uint64_t* p_empty = p_full + kTgPacked;
+  uint64_t* acc_full = p_empty + kTgPacked;   // [2]
+  uint64_t* acc_empty = acc_full + 2;         // [2]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
   int* s_off = reinterpret_cast<int*>(s_tmem + 4);
   int* s_first = s_off + p.grp.experts + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nkb = p.K / 128;
+  const int nkb = p.K / 128;            // 128-position blocks
+  const int nst = (nkb + 1) / 2;        // stages of 256 positions
   const int row_tiles = (p.N + kTgBM - 1) / kTgBM;
 
   if (tid == 0) {
     for (int s = 0; s < kTgStages; ++s) {
-      mbar_init(&full[s], kTcProducers / 32 + 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
+    }
+    for (int s = 0; s < kTgSlots; ++s) {
+      mbar_init(&a_full[s], 4);   // the four warps of the group that filled it
+      mbar_init(&a_empty[s], 1);
+    }
+    for (int s = 0; s < kTgPacked; ++s) {
+      mbar_init(&p_full[s], 1);
+      mbar_init(&p_empty[s], kTcProducers / 32);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], kTcEpilogue / 32);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tmap_x64);
+    tma_prefetch_map(&tmap_x16);
+    tma_prefetch_map(&tmap_c);
+    if (!DENSE) tma_prefetch_map(&tmap_m);
+    if (p.aligned) tma_prefetch_map(&tmap_y);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(s_tmem)),
@@ -154,28 +205,52 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   int used = 0;   // tiles this role has worked on
 
   if (warp == 0) {
-    // ---- TMA of the activation rows ----
+    // ---- TMA of the activation rows (a half stage's second block: zeros) ----
     if (lane == 0) {
       int it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
         const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
         if (!t.nmma) continue;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
+        for (int ks = 0; ks < nst; ++ks, ++it) {
           const int s = it % kTgStages;
-          if (!mbar_wait(&empty[s], ((it / kTgStages) & 1u) ^ 1u)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[s], (uint32_t)t.nmma * 128u);
-          uint8_t* dst = smem + (size_t)s * kTgStageBytes + kTgABytes;
-          int r = 0;
-          for (; r + 64 <= t.nmma; r += 64) tma_load_2d(dst + r * 128, &tmap_x64, kb * 128, t.tok0 + r, &full[s]);
-          for (; r < t.nmma; r += 16) tma_load_2d(dst + r * 128, &tmap_x16, kb * 128, t.tok0 + r, &full[s]);
+          if (!mbar_wait(&b_empty[s], ((it / kTgStages) & 1u) ^ 1u)) { ok = false; break; }
+          mbar_arrive_expect_tx(&b_full[s], (uint32_t)t.nmma * 256u);
+          uint8_t* dst = smem + (size_t)s * kTgStageBytes;
+#pragma unroll
+          for (int j = 0; j < 2; ++j, dst += kTgSub) {
+            const int x = ks * 256 + j * 128;
+            int r = 0;
+            for (; r + 64 <= t.nmma; r += 64) tma_load_2d(dst + r * 128, &tmap_x64, x, t.tok0 + r, &b_full[s]);
+            for (; r < t.nmma; r += 16) tma_load_2d(dst + r * 128, &tmap_x16, x, t.tok0 + r, &b_full[s]);
+          }
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ---- TMA of the packed rows ----
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
+        const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
+        if (!t.nmma) continue;
+        const int row = t.e * p.N + t.row0;   // rows past the expert's are expanded, never stored
+        for (int ks = 0; ks < nst; ++ks, ++it) {
+          const int s = it % kTgPacked;
+          if (!mbar_wait(&p_empty[s], ((it / kTgPacked) & 1u) ^ 1u)) { ok = false; break; }
+          uint8_t* dst = packed + s * kTgPackedBytes;
+          mbar_arrive_expect_tx(&p_full[s], (uint32_t)(kTgBM * (16 * CB + (DENSE ? 0 : 32))));
+          tma_load_2d(dst, &tmap_c, ks * 16 * CB, row, &p_full[s]);
+          if (!DENSE) tma_load_2d(dst + kTgBM * 64, &tmap_m, ks * 32, row, &p_full[s]);
         }
       }
     }
   } else if (warp == 1) {
     // ---- MMA issuer ----
     if (lane == 0) {
-      int it = 0;
+      const uint64_t bdesc0 = sw128_kmajor_desc(smem_u32(smem));
+      int it = 0, blk = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
         const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
@@ -183,18 +258,24 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         const uint32_t idesc = kTgIdesc0 | ((uint32_t)(t.nmma >> 3) << 17);
         const int b = used & 1;
         if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
-        tc_fence_after();
         const uint32_t d_tmem = tmem + (uint32_t)(b * kTgBN);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % kTgStages;
-          if (!mbar_wait(&full[s], (it / kTgStages) & 1u)) { ok = false; break; }
+        for (int kb = 0; kb < nkb; ++kb, ++blk) {
+          const int s = it % kTgStages, a = blk % kTgSlots;
+          const uint32_t pb = (it / kTgStages) & 1u, pa = (blk / kTgSlots) & 1u;
+          if (!(kb & 1) && !mbar_test(&b_full[s], pb) && !mbar_wait(&b_full[s], pb)) { ok = false; break; }
+          if (!mbar_test(&a_full[a], pa) && !mbar_wait(&a_full[a], pa)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + (size_t)s * kTgStageBytes);
-          const uint64_t adesc = sw128_kmajor_desc(a_addr), bdesc = sw128_kmajor_desc(a_addr + kTgABytes);
+          const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgStageBytes / 16) + (kb & 1) * (kTgSub / 16));
+          const uint32_t a_tmem = tmem + kTgACol + 32u * (uint32_t)a;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_i8_n(d_tmem, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)(2 * k), idesc, (kb > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&empty[s]);
+            tc_mma_i8_ta(d_tmem, a_tmem + 8u * (uint32_t)k, bdesc + (uint64_t)(2 * k), idesc,
+                         (kb > 0 || k > 0) ? 1u : 0u);
+          tc_commit(&a_empty[a]);
+          if ((kb & 1) || kb + 1 == nkb) {
+            tc_commit(&b_empty[s]);
+            ++it;
+          }
         }
         tc_commit(&acc_full[b]);
         ++used;
@@ -205,59 +286,59 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
-    // ---- producers: thread (i, h) expands positions 64 h .. of row i ----
-    const int pi = tid - 128, i = pi & 127, h = pi >> 7;
+    // ---- producers: thread = feature 32 q + lane; group g takes the blocks
+    // with index = g (mod 2), counted over all tiles ----
+    const int q = warp & 3, g = (warp - 4) >> 2;
+    const int i = 32 * q + lane;
     const uint2* sel = s_sel + (lane & (kTgSelCopies - 1));
-    int it = 0;
+    const uint32_t a_base = tmem + kTgACol + ((uint32_t)(32 * q) << 16);
+    int it = 0, blk = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
       const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
       if (!t.nmma) continue;
-      const int row = min(t.row0 + i, p.N - 1);   // rows past N repeat the last one; not stored
-      const size_t wrow = (size_t)t.e * p.N + row;
-      const uint8_t* crow = p.codes + wrow * p.cstride + h * 4 * CB;
-      const uint8_t* mrow = DENSE ? nullptr : p.meta + wrow * p.mstride + h * 8;
-      uint32_t cn[CB], mn[2] = {0u, 0u};
-      auto load = [&](int kb) {
-        if (kb < nkb) {
-          const uint32_t* cp = reinterpret_cast<const uint32_t*>(crow + (size_t)kb * 8 * CB);
+      for (int ks = 0; ks < nst && ok; ++ks, ++it) {
+        const int ps = it % kTgPacked;
+        if (!mbar_wait(&p_full[ps], (it / kTgPacked) & 1u)) { ok = false; break; }
+        const int nsub = 2 * ks + 1 < nkb ? 2 : 1;
+        // which of the stage's blocks is this group's (none in a half stage of the other's)
+        const int sub = (blk & 1) == g ? 0 : 1;
+        const int mine = blk + sub;
+        blk += nsub;
+        uint32_t w[32];
+        if (sub < nsub) {
+          const uint8_t* cp = packed + ps * kTgPackedBytes + i * 16 * CB + sub * 8 * CB;
+          uint32_t cw[2][CB], mw[2][2] = {{0u, 0u}, {0u, 0u}};
 #pragma unroll
-          for (int q = 0; q < CB; ++q) cn[q] = __ldg(cp + q);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < CB; ++j) cw[h][j] = reinterpret_cast<const uint32_t*>(cp)[h * CB + j];
           if (!DENSE) {
-            const uint2 m = __ldg(reinterpret_cast<const uint2*>(mrow + (size_t)kb * 16));
-            mn[0] = m.x;
-            mn[1] = m.y;
+            const uint4 m = *reinterpret_cast<const uint4*>(packed + ps * kTgPackedBytes + kTgBM * 64 + i * 32 + sub * 16);
+            mw[0][0] = m.x; mw[0][1] = m.y; mw[1][0] = m.z; mw[1][1] = m.w;
           }
+          tg_expand64<MM, CB, DENSE>(cw[0], mw[0], sel, w);
+          tg_expand64<MM, CB, DENSE>(cw[1], mw[1], sel, w + 16);
         }
-      };
-      load(0);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int s = it % kTgStages;
-        uint32_t cw[CB], mw[2] = {mn[0], mn[1]};
-#pragma unroll
-        for (int q = 0; q < CB; ++q) cw[q] = cn[q];
-        load(kb + 1);
-        uint32_t w[16];
-        tg_expand64<MM, CB, DENSE>(cw, mw, sel, w);
-        int got = 1;
-        if (lane == 0) got = mbar_wait(&empty[s], ((it / kTgStages) & 1u) ^ 1u) ? 1 : 0;
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) { ok = false; break; }
-        uint8_t* arow = smem + (size_t)s * kTgStageBytes + (size_t)i * 128;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(arow + (((4 * h + u) ^ (i & 7)) << 4)) =
-              make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        if (lane == 0) mbar_arrive(&p_empty[ps]);
+        if (sub < nsub) {
+          const int a = mine % kTgSlots;
+          if (!mbar_wait(&a_empty[a], ((mine / kTgSlots) & 1u) ^ 1u)) { ok = false; break; }
+          tc_fence_after();
+          tmem_st32(a_base + 32u * (uint32_t)a, w);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&a_full[a]);
+        }
       }
     }
   } else if (warp >= 12) {
     // ---- epilogue ----
     const int q = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-    EpiTile et{reinterpret_cast<uint16_t*>(ybuf + (size_t)(warp - 12) * 4096), 0};
+    EpiTile et{reinterpret_cast<uint16_t*>(ybuf + (size_t)(warp - 12) * 4096),
+               reinterpret_cast<float*>(ybuf + (kTcEpilogue / 32) * 4096) + 32 * (warp - 12), 0};
     const EpiOut out{&tmap_y, &tmap_z, p.y, p.N, p.grp.rows, p.aligned != 0};
     for (int tile = blockIdx.x; tile < n_tiles; tile += grid) {
       const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
@@ -269,6 +350,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       const int chunks = (t.tok_end - t.tok0 + 31) / 32;
       uint4 res[4];
       epi_load_residual(p.ep, out, row_w, t.tok0, t.tok_end, lane, res);
+      float xs_n = t.tok0 + lane < t.tok_end ? __ldg(p.xs + t.tok0 + lane) : 0.f;
       int got = 1;
       if (lane == 0) got = mbar_wait(&acc_full[b], (used >> 1) & 1u) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
@@ -278,14 +360,18 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int tok = t.tok0 + 32 * c;
-        const float sc = tok + lane < t.tok_end ? __fdiv_rn(__fmul_rn(gm, __ldg(p.xs + tok + lane)), 127.0f) : 0.f;
         uint32_t r[32];
-        tmem_ld32(tmem + lane_base + (uint32_t)(b * kTgBN + 32 * c), r);
+        tmem_ld32_issue(tmem + lane_base + (uint32_t)(b * kTgBN + 32 * c), r);
+        const float sc = __fdiv_rn(__fmul_rn(gm, xs_n), 127.0f);
+        xs_n = tok + 32 + lane < t.tok_end ? __ldg(p.xs + tok + 32 + lane) : 0.f;
+        tmem_ld_wait(r);
+        if (c + 1 == chunks) {   // the accumulator is in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
         epi_chunk(p.ep, out, et, r, sc, bias, row_w, tok, t.tok_end, c + 1 < chunks ? tok + 32 : -1, lane, res);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
     }
     if (lane == 0) tma_store_wait_all();
     griddep_launch_dependents();

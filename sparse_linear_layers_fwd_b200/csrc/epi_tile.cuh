@@ -19,6 +19,7 @@ namespace sbn {
 
 struct EpiTile {
   uint16_t* buf;     // this warp's two 32 x 32 tiles
+  float* sc;         // and 32 floats
   int nstore;        // TMA stores so far (the tile to use next without z)
 };
 
@@ -60,10 +61,20 @@ SBN_DEVFN void epi_store_rows(uint16_t* dst, const uint16_t* tile, int N, int ro
 // is this chunk's residual and is reloaded for the next one (next_tok < 0: none).
 SBN_DEVFN void epi_chunk(const EpiParams& ep, const EpiOut& o, EpiTile& t, const uint32_t (&r)[32], float sc, float bias,
                          int row_w, int tok, int tok_end, int next_tok, int lane, uint4 (&res)[4]) {
+  // the tokens' factors by 16-byte broadcast reads (a shuffle per element
+  // cost as much as the rest of a plain epilogue)
   float v[32];
+  t.sc[lane] = sc;
+  __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    v[j] = __fadd_rn(__fmul_rn((float)(int32_t)r[j], __shfl_sync(0xffffffffu, sc, j)), bias);
+  for (int j = 0; j < 8; ++j) {
+    const float4 f = reinterpret_cast<const float4*>(t.sc)[j];
+    v[4 * j] = __fmaf_rn((float)(int32_t)r[4 * j], f.x, bias);
+    v[4 * j + 1] = __fmaf_rn((float)(int32_t)r[4 * j + 1], f.y, bias);
+    v[4 * j + 2] = __fmaf_rn((float)(int32_t)r[4 * j + 2], f.z, bias);
+    v[4 * j + 3] = __fmaf_rn((float)(int32_t)r[4 * j + 3], f.w, bias);
+  }
+  __syncwarp();
   const int row = row_w + lane;
   if (!o.aligned) {
     if (ep.z) {

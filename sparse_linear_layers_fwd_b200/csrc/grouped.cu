@@ -86,11 +86,18 @@ struct LaunchTc {
     static bool attr_set[kMaxDevices] = {};
     auto kern = bl_tc_grp_kernel<MM, CB, DENSE>;
     if (!set_smem_attr_once(kern, tg_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
-    CUtensorMap x64, x16, ty, tz;
+    CUtensorMap x64, x16, tc, tm, ty, tz;
     if (!encode_2d(&x64, CU_TENSOR_MAP_DATA_TYPE_UINT8, f.xq, f.k, f.grp.rows, f.k, 128, 64,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&x16, CU_TENSOR_MAP_DATA_TYPE_UINT8, f.xq, f.k, f.grp.rows, f.k, 128, 16,
                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return SBN_ERR_CUDA;
+    const uint64_t wrows = (uint64_t)f.grp.experts * (uint64_t)f.n_out;
+    tm = x64;   // unused for n == m
+    if (!encode_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, f.codes, f.cstride(), wrows, f.cstride(), 16 * CB, kTgBM,
+                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        (!DENSE && !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, f.meta, f.mstride(), wrows, f.mstride(), 32, kTgBM,
+                              CU_TENSOR_MAP_SWIZZLE_NONE)))
       return SBN_ERR_CUDA;
     TgParams p;
     p.codes = f.codes; p.meta = f.meta; p.xs = f.xs; p.gamma = f.gamma; p.y = f.y; p.ep = f.ep; p.grp = f.grp;
@@ -105,12 +112,12 @@ struct LaunchTc {
                                 CU_TENSOR_MAP_SWIZZLE_NONE)))
         return SBN_ERR_CUDA;
     }
-    // tiles: at most one more than rows / 256 per expert, for every block of features
+    // tiles: at most one more than rows / kTgBN per expert, for every block of features
     const long long row_tiles = (f.n_out + kTgBM - 1) / kTgBM;
     const long long most = (f.grp.rows / kTgBN + std::min(f.grp.experts, f.grp.rows)) * row_tiles;
     const int grid = (int)std::max(1LL, std::min(most, (long long)f.sms));
-    return launch_ex(kern, dim3((unsigned)grid), dim3(kTcThreads), tg_smem_bytes(f.grp.experts), f.st, 1, x64, x16, ty,
-                     tz, p);
+    return launch_ex(kern, dim3((unsigned)grid), dim3(kTcThreads), tg_smem_bytes(f.grp.experts), f.st, 1, x64, x16, tc,
+                     tm, ty, tz, p);
   }
 };
 

@@ -114,6 +114,7 @@ def test_adamw_validation(sbn_lib):
     assert adamw_call(lib, b1=1.0) == 2
     assert adamw_call(lib, b2=-0.1) == 2
     assert adamw_call(lib, eps=-1.0) == 2
+    assert adamw_call(lib, eps=0.0) == 2
     assert adamw_call(lib, eps=float("nan")) == 2
     assert adamw_call(lib, lr=float("inf")) == 2
     assert adamw_call(lib, with_(6, A), pb=1) == 2          # no copy of bf16 parameters
