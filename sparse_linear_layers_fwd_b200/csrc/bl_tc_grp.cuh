@@ -7,7 +7,7 @@
 // bias_e) + residual. Without offsets it is one layer over all rows.
 //
 // A persistent CTA per SM walks the tiles of the work list (grp.cuh): 128
-// output features x up to 192 rows of one expert, an expert's rows split into
+// output features x up to 160 rows of one expert, an expert's rows split into
 // equal tiles (a multiple of 16 rows each, the MMA's N). The packed weights
 // are read once per tile and expanded on the way to the MMA, since an expert
 // sees few rows: expanding them in memory first would cost as much as the
@@ -22,13 +22,22 @@
 //   warp 1      TMEM allocation and the MMA thread;
 //   warp 2      the work list, then TMA of the packed rows (codes and keep
 //               bits of 128 features x 256 positions) into a ring of their own;
-//   warps 4-11  producers: two groups of four warps take 128-position blocks
-//               in turn; a thread expands its feature's block (bl_gemv.cuh's
-//               expansion) into 32 registers, one tcgen05.st;
-//   warps 12-15 epilogue (epi_tile.cuh).
-// TMEM: two accumulators of 192 columns, four A slots of 32 columns. Rows of
-// the next expert that share a box are loaded and multiplied, never stored.
-// All waits are bounded in time.
+//   warps 4-15  producers: three groups of four warps, one for each stage of
+//               the ring; a thread expands its feature's 256 positions
+//               (bl_gemv.cuh's expansion), 32 registers per tcgen05.st;
+//   warps 16-19 epilogue (epi_tile.cuh).
+// The loops of the MMA and TMA warps are run by whole warps and only the
+// instructions themselves by one elected lane: addresses and descriptors then
+// live in uniform registers, and eight MMAs are issued in 190 cycles instead
+// of 840. Every lane waits on a barrier itself, which is faster than one lane
+// and a shuffle.
+// One ring of three stages serves both operands (TMEM: two accumulators of
+// 160 columns, three A slots of 64): one barrier to wait for and one commit
+// per stage, since what the MMA thread does between two stages leaves the
+// tensor pipe idle (with separate rings of three activation stages and two A
+// slots behind 192-column accumulators, 340 of 1070 cycles). Rows of the next
+// expert that share a box are loaded and multiplied, never stored. All waits
+// are bounded in time.
 #pragma once
 
 #include <cuda.h>
@@ -43,23 +52,25 @@
 namespace sbn {
 
 constexpr int kTgBM = 128;
-constexpr int kTgBN = 192;
-constexpr int kTgStages = 3;                   // activation stages of 256 positions
-constexpr int kTgSub = kTgBN * 128;            // one 128-position block of a stage
+constexpr int kTgBN = 160;
+constexpr int kTgStages = 3;                   // stages of 256 positions
+constexpr int kTgSub = kTgBN * 128;            // activations of one 128-position block
 constexpr int kTgStageBytes = 2 * kTgSub;
-constexpr int kTgSlots = 4;                    // A slots in TMEM
-constexpr uint32_t kTgACol = 2 * kTgBN;
-static_assert(kTgACol + 32 * kTgSlots <= kTcTmemCols, "accumulators and A slots fit in TMEM");
-constexpr int kTgPacked = 4;                   // packed stages of 256 positions
-constexpr int kTgPackedBytes = kTgBM * (64 + 32);
+constexpr uint32_t kTgACol = 2 * kTgBN;        // A slots after the accumulators
+static_assert(kTgACol + 64 * kTgStages <= kTcTmemCols, "accumulators and A slots fit in TMEM");
+static_assert(kTgSub % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
+constexpr int kTgPackedBytes = kTgBM * (64 + 32);   // packed rows of a stage
+constexpr int kTgThreads = 640;
+constexpr int kTgEpiWarp = 16;                 // first epilogue warp
 constexpr int kTgSelCopies = 4;
 constexpr int kTgYBuf = (kTcEpilogue / 32) * (4096 + 128);
-constexpr int kTgBars = 2 * (kTgStages + kTgSlots + kTgPacked) + 4;
+constexpr int kTgBars = 4 * kTgStages + 4;
+constexpr int kTgList = 256;                   // tiles of a CTA whose place is worked out ahead
 constexpr uint32_t kTgIdesc0 = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTgBM >> 4) << 24);
 
 __host__ __device__ inline size_t tg_smem_bytes(int experts) {
-  return 1024 + (size_t)kTgStages * kTgStageBytes + kTgPacked * kTgPackedBytes + kTgYBuf + 256 * 8 * kTgSelCopies +
-         kTgBars * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
+  return 1024 + (size_t)kTgStages * (kTgStageBytes + kTgPackedBytes) + kTgYBuf + 256 * 8 * kTgSelCopies +
+         kTgBars * 8 + 16 + 16 * kTgList + 2 * 4 * (size_t)(experts + 1);
 }
 
 struct TgParams {
@@ -97,6 +108,11 @@ SBN_DEVFN TgTile tg_tile(const int* off, const int* first, const GrpParams& g, i
   return t;
 }
 
+SBN_DEVFN bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0u;
+}
 // A from tensor memory, B from shared memory.
 SBN_DEVFN void tc_mma_i8_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -118,6 +134,15 @@ SBN_DEVFN void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
+// The k-th tile of this CTA: from the list, worked out on the spot behind it.
+SBN_DEVFN TgTile tg_get(const int4* list, const int* off, const int* first, const GrpParams& g, int k, int row_tiles) {
+  if (k >= kTgList)
+    return tg_tile(off, first, g, (int)blockIdx.x + k * (int)gridDim.x, row_tiles, kTgBM, kTgBN, 16);
+  const int4 v = list[k];
+  const int have = v.w - v.z;
+  return TgTile{v.x, v.y, v.z, v.w, have > 0 ? (have + 15) / 16 * 16 : 0};
+}
+
 // 64 positions (one span of bl_gemv.cuh) -> 16 words of int8.
 template <int MM, int CB, bool DENSE>
 SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* sel, uint32_t* w) {
@@ -132,7 +157,7 @@ SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], co
 }
 
 template <int MM, int CB, bool DENSE>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTgThreads, 1)
 bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_constant__ CUtensorMap tmap_x16,
                  const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_m,
                  const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_z,
@@ -140,18 +165,17 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* packed = smem + (size_t)kTgStages * kTgStageBytes;
-  uint8_t* ybuf = packed + kTgPacked * kTgPackedBytes;
+  uint8_t* ybuf = packed + kTgStages * kTgPackedBytes;
   uint2* s_sel = reinterpret_cast<uint2*>(ybuf + kTgYBuf);   // [256][kTgSelCopies]
-  uint64_t* b_full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
-  uint64_t* b_empty = b_full + kTgStages;
-  uint64_t* a_full = b_empty + kTgStages;
-  uint64_t* a_empty = a_full + kTgSlots;
-  uint64_t* p_full = a_empty + kTgSlots;
-  uint64_t* p_empty = p_full + kTgPacked;
-  uint64_t* acc_full = p_empty + kTgPacked;   // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
+  uint64_t* empty = full + kTgStages;
+  uint64_t* p_full = empty + kTgStages;
+  uint64_t* p_empty = p_full + kTgStages;
+  uint64_t* acc_full = p_empty + kTgStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;         // [2]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
-  int* s_off = reinterpret_cast<int*>(s_tmem + 4);
+  int4* s_list = reinterpret_cast<int4*>(s_tmem + 4);
+  int* s_off = reinterpret_cast<int*>(s_list + kTgList);
   int* s_first = s_off + p.grp.experts + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -161,16 +185,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
 
   if (tid == 0) {
     for (int s = 0; s < kTgStages; ++s) {
-      mbar_init(&b_full[s], 1);
-      mbar_init(&b_empty[s], 1);
-    }
-    for (int s = 0; s < kTgSlots; ++s) {
-      mbar_init(&a_full[s], 4);   // the four warps of the group that filled it
-      mbar_init(&a_empty[s], 1);
-    }
-    for (int s = 0; s < kTgPacked; ++s) {
+      mbar_init(&full[s], 4 + 1);   // the stage's producer warps and the activations' TMA
+      mbar_init(&empty[s], 1);
       mbar_init(&p_full[s], 1);
-      mbar_init(&p_empty[s], kTcProducers / 32);
+      mbar_init(&p_empty[s], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -201,147 +219,181 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const int n_tiles = s_first[p.grp.experts];
-  const int grid = (int)gridDim.x;
+  const int count = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  for (int k = tid; k < min(count, kTgList); k += kTgThreads) {
+    const TgTile t = tg_tile(s_off, s_first, p.grp, (int)blockIdx.x + k * (int)gridDim.x, row_tiles, kTgBM, kTgBN, 16);
+    s_list[k] = make_int4(t.e, t.row0, t.tok0, t.tok_end);
+  }
+  __syncthreads();
   int used = 0;   // tiles this role has worked on
 
   if (warp == 0) {
     // ---- TMA of the activation rows (a half stage's second block: zeros) ----
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-        const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
-        if (!t.nmma) continue;
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          const int s = it % kTgStages;
-          if (!mbar_wait(&b_empty[s], ((it / kTgStages) & 1u) ^ 1u)) { ok = false; break; }
-          mbar_arrive_expect_tx(&b_full[s], (uint32_t)t.nmma * 256u);
-          uint8_t* dst = smem + (size_t)s * kTgStageBytes;
+    const bool lead = elect_one();
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      if (!t.nmma) continue;
+      const int nmma = __shfl_sync(0xffffffffu, t.nmma, 0), tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        uint8_t* dst = smem + (size_t)s * kTgStageBytes;
+        if (lead) {
+          mbar_arrive_expect_tx(&full[s], (uint32_t)nmma * 256u);
 #pragma unroll
-          for (int j = 0; j < 2; ++j, dst += kTgSub) {
+          for (int j = 0; j < 2; ++j) {
             const int x = ks * 256 + j * 128;
             int r = 0;
-            for (; r + 64 <= t.nmma; r += 64) tma_load_2d(dst + r * 128, &tmap_x64, x, t.tok0 + r, &b_full[s]);
-            for (; r < t.nmma; r += 16) tma_load_2d(dst + r * 128, &tmap_x16, x, t.tok0 + r, &b_full[s]);
+            for (; r + 64 <= nmma; r += 64) tma_load_2d(dst + j * kTgSub + r * 128, &tmap_x64, x, tok0 + r, &full[s]);
+            for (; r < nmma; r += 16) tma_load_2d(dst + j * kTgSub + r * 128, &tmap_x16, x, tok0 + r, &full[s]);
           }
+        }
+        __syncwarp();
+        if (++s == kTgStages) {
+          s = 0;
+          ph ^= 1u;
         }
       }
     }
   } else if (warp == 2) {
     // ---- TMA of the packed rows ----
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-        const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
-        if (!t.nmma) continue;
-        const int row = t.e * p.N + t.row0;   // rows past the expert's are expanded, never stored
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          const int s = it % kTgPacked;
-          if (!mbar_wait(&p_empty[s], ((it / kTgPacked) & 1u) ^ 1u)) { ok = false; break; }
-          uint8_t* dst = packed + s * kTgPackedBytes;
+    const bool lead = elect_one();
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      if (!t.nmma) continue;
+      // rows past the expert's are expanded, never stored
+      const int row = __shfl_sync(0xffffffffu, t.e * p.N + t.row0, 0);
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&p_empty[s], ph)) { ok = false; break; }
+        uint8_t* dst = packed + s * kTgPackedBytes;
+        if (lead) {
           mbar_arrive_expect_tx(&p_full[s], (uint32_t)(kTgBM * (16 * CB + (DENSE ? 0 : 32))));
           tma_load_2d(dst, &tmap_c, ks * 16 * CB, row, &p_full[s]);
           if (!DENSE) tma_load_2d(dst + kTgBM * 64, &tmap_m, ks * 32, row, &p_full[s]);
         }
+        __syncwarp();
+        if (++s == kTgStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
     }
   } else if (warp == 1) {
-    // ---- MMA issuer ----
-    if (lane == 0) {
-      const uint64_t bdesc0 = sw128_kmajor_desc(smem_u32(smem));
-      int it = 0, blk = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-        const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
-        if (!t.nmma) continue;
-        const uint32_t idesc = kTgIdesc0 | ((uint32_t)(t.nmma >> 3) << 17);
-        const int b = used & 1;
-        if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
-        const uint32_t d_tmem = tmem + (uint32_t)(b * kTgBN);
-        for (int kb = 0; kb < nkb; ++kb, ++blk) {
-          const int s = it % kTgStages, a = blk % kTgSlots;
-          const uint32_t pb = (it / kTgStages) & 1u, pa = (blk / kTgSlots) & 1u;
-          if (!(kb & 1) && !mbar_test(&b_full[s], pb) && !mbar_wait(&b_full[s], pb)) { ok = false; break; }
-          if (!mbar_test(&a_full[a], pa) && !mbar_wait(&a_full[a], pa)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgStageBytes / 16) + (kb & 1) * (kTgSub / 16));
-          const uint32_t a_tmem = tmem + kTgACol + 32u * (uint32_t)a;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_i8_ta(d_tmem, a_tmem + 8u * (uint32_t)k, bdesc + (uint64_t)(2 * k), idesc,
-                         (kb > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&a_empty[a]);
-          if ((kb & 1) || kb + 1 == nkb) {
-            tc_commit(&b_empty[s]);
-            ++it;
-          }
-        }
-        tc_commit(&acc_full[b]);
-        ++used;
-      }
-      // the last commits before TMEM is freed (also on the abort path)
-      for (int j = used - 2; j < used; ++j)
-        if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
-    }
-    __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
-    // ---- producers: thread = feature 32 q + lane; group g takes the blocks
-    // with index = g (mod 2), counted over all tiles ----
-    const int q = warp & 3, g = (warp - 4) >> 2;
-    const int i = 32 * q + lane;
-    const uint2* sel = s_sel + (lane & (kTgSelCopies - 1));
-    const uint32_t a_base = tmem + kTgACol + ((uint32_t)(32 * q) << 16);
-    int it = 0, blk = 0;
+    // ---- MMA issuer: the whole warp runs the loop (addresses and descriptors
+    // stay in uniform registers), one elected lane issues ----
+    const bool lead = elect_one();
+    const uint64_t bdesc0 = sw128_kmajor_desc(smem_u32(smem));
+    int s = 0;
+    uint32_t ph = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-      const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
-      if (!t.nmma) continue;
-      for (int ks = 0; ks < nst && ok; ++ks, ++it) {
-        const int ps = it % kTgPacked;
-        if (!mbar_wait(&p_full[ps], (it / kTgPacked) & 1u)) { ok = false; break; }
-        const int nsub = 2 * ks + 1 < nkb ? 2 : 1;
-        // which of the stage's blocks is this group's (none in a half stage of the other's)
-        const int sub = (blk & 1) == g ? 0 : 1;
-        const int mine = blk + sub;
-        blk += nsub;
-        uint32_t w[32];
-        if (sub < nsub) {
-          const uint8_t* cp = packed + ps * kTgPackedBytes + i * 16 * CB + sub * 8 * CB;
-          uint32_t cw[2][CB], mw[2][2] = {{0u, 0u}, {0u, 0u}};
+    TgTile t = count ? tg_get(s_list, s_off, s_first, p.grp, 0, row_tiles) : TgTile{};
+    for (int k = 0; k < count && ok; ++k) {
+      const int nmma = t.nmma;
+      if (k + 1 < count) t = tg_get(s_list, s_off, s_first, p.grp, k + 1, row_tiles);
+      if (!nmma) continue;
+      const uint32_t idesc = __shfl_sync(0xffffffffu, kTgIdesc0 | ((uint32_t)(nmma >> 3) << 17), 0);
+      const int b = used & 1;
+      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      const uint32_t d_tmem = tmem + (uint32_t)(b * kTgBN);
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgStageBytes / 16));
+        const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)s;
+        if (lead) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < 4; ++i)
+            tc_mma_i8_ta(d_tmem, a_tmem + 8u * (uint32_t)i, bdesc + (uint64_t)(2 * i), idesc, (ks > 0 || i > 0) ? 1u : 0u);
+          if (2 * ks + 1 < nkb) {
 #pragma unroll
-            for (int j = 0; j < CB; ++j) cw[h][j] = reinterpret_cast<const uint32_t*>(cp)[h * CB + j];
-          if (!DENSE) {
-            const uint4 m = *reinterpret_cast<const uint4*>(packed + ps * kTgPackedBytes + kTgBM * 64 + i * 32 + sub * 16);
-            mw[0][0] = m.x; mw[0][1] = m.y; mw[1][0] = m.z; mw[1][1] = m.w;
+            for (int i = 0; i < 4; ++i)
+              tc_mma_i8_ta(d_tmem, a_tmem + 32u + 8u * (uint32_t)i, bdesc + (uint64_t)(kTgSub / 16 + 2 * i), idesc, 1u);
           }
-          tg_expand64<MM, CB, DENSE>(cw[0], mw[0], sel, w);
-          tg_expand64<MM, CB, DENSE>(cw[1], mw[1], sel, w + 16);
+          tc_commit(&empty[s]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_empty[ps]);
-        if (sub < nsub) {
-          const int a = mine % kTgSlots;
-          if (!mbar_wait(&a_empty[a], ((mine / kTgSlots) & 1u) ^ 1u)) { ok = false; break; }
-          tc_fence_after();
-          tmem_st32(a_base + 32u * (uint32_t)a, w);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&a_full[a]);
+        if (++s == kTgStages) {
+          s = 0;
+          ph ^= 1u;
         }
       }
+      if (lead) tc_commit(&acc_full[b]);
+      __syncwarp();
+      ++used;
     }
-  } else if (warp >= 12) {
+    // the last commits before TMEM is freed (also on the abort path)
+    for (int j = used - 2; j < used; ++j)
+      if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
+    __syncwarp();
+  } else if (warp >= 4 && warp < kTgEpiWarp) {
+    // ---- producers: thread = feature 32 q + lane, group g = stage of the ring
+    // (a half stage's second block: zeros, not multiplied) ----
+    const int q = warp & 3, s = (warp - 4) >> 2;
+    const int i = 32 * q + lane;
+    const uint2* sel = s_sel + (lane & (kTgSelCopies - 1));
+    const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)s + ((uint32_t)(32 * q) << 16);
+    const uint2* cp = reinterpret_cast<const uint2*>(packed + s * kTgPackedBytes + i * 16 * CB);
+    const uint4* mp = reinterpret_cast<const uint4*>(packed + s * kTgPackedBytes + kTgBM * 64 + i * 32);
+    int it = 0;   // stages over all tiles
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      if (!t.nmma) continue;
+      // this group's stages of the tile
+      const int end = it + nst;
+      int mine = it + (s - it % kTgStages + kTgStages) % kTgStages;
+      it = end;
+      for (; mine < end; mine += kTgStages, ph ^= 1u) {
+        if (!mbar_wait(&p_full[s], ph)) { ok = false; break; }
+        uint2 cv[2 * CB];
+        uint4 mv[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+#pragma unroll
+        for (int j = 0; j < 2 * CB; ++j) cv[j] = cp[j];
+        if (!DENSE) {
+          mv[0] = mp[0];
+          mv[1] = mp[1];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_empty[s]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t cw[2][CB];
+#pragma unroll
+          for (int h = 0; h < 2 * CB; ++h) {
+            const uint2 c2 = cv[(2 * CB * j + h) / 2];
+            cw[h / CB][h % CB] = ((2 * CB * j + h) & 1) ? c2.y : c2.x;
+          }
+          const uint32_t m0[2] = {mv[j].x, mv[j].y}, m1[2] = {mv[j].z, mv[j].w};
+          uint32_t w[32];
+          tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
+          tg_expand64<MM, CB, DENSE>(cw[1], m1, sel, w + 16);
+          if (j == 0) {
+            if (!mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+            tc_fence_after();
+          }
+          tmem_st32(a_tmem + 32u * (uint32_t)j, w);
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+      }
+    }
+  } else if (warp >= kTgEpiWarp) {
     // ---- epilogue ----
     const int q = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-    EpiTile et{reinterpret_cast<uint16_t*>(ybuf + (size_t)(warp - 12) * 4096),
-               reinterpret_cast<float*>(ybuf + (kTcEpilogue / 32) * 4096) + 32 * (warp - 12), 0};
+    EpiTile et{reinterpret_cast<uint16_t*>(ybuf + (size_t)(warp - kTgEpiWarp) * 4096),
+               reinterpret_cast<float*>(ybuf + (kTcEpilogue / 32) * 4096) + 32 * (warp - kTgEpiWarp), 0};
     const EpiOut out{&tmap_y, &tmap_z, p.y, p.N, p.grp.rows, p.aligned != 0};
-    for (int tile = blockIdx.x; tile < n_tiles; tile += grid) {
-      const TgTile t = tg_tile(s_off, s_first, p.grp, tile, row_tiles, kTgBM, kTgBN, 16);
+    for (int k = 0; k < count; ++k) {
+      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       const int b = used & 1;
       const int row_w = t.row0 + 32 * q;
@@ -351,10 +403,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       uint4 res[4];
       epi_load_residual(p.ep, out, row_w, t.tok0, t.tok_end, lane, res);
       float xs_n = t.tok0 + lane < t.tok_end ? __ldg(p.xs + t.tok0 + lane) : 0.f;
-      int got = 1;
-      if (lane == 0) got = mbar_wait(&acc_full[b], (used >> 1) & 1u) ? 1 : 0;
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) break;
+      if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1

@@ -116,7 +116,7 @@ struct LaunchTc {
     const long long row_tiles = (f.n_out + kTgBM - 1) / kTgBM;
     const long long most = (f.grp.rows / kTgBN + std::min(f.grp.experts, f.grp.rows)) * row_tiles;
     const int grid = (int)std::max(1LL, std::min(most, (long long)f.sms));
-    return launch_ex(kern, dim3((unsigned)grid), dim3(kTcThreads), tg_smem_bytes(f.grp.experts), f.st, 1, x64, x16, tc,
+    return launch_ex(kern, dim3((unsigned)grid), dim3(kTgThreads), tg_smem_bytes(f.grp.experts), f.st, 1, x64, x16, tc,
                      tm, ty, tz, p);
   }
 };
