@@ -337,7 +337,7 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
 #pragma unroll
       for (int cc = 0; cc < NCH; ++cc) {
         const int my_tok = tok0 + 32 * (c_first + cc) + lane;
-        scq[cc] = (ACC || cc >= nch || my_tok >= p.T) ? 0.f : __fdiv_rn(__fmul_rn(g, __ldg(p.xs + my_tok)), 127.0f);
+        scq[cc] = (ACC || EPI || cc >= nch || my_tok >= p.T) ? 0.f : __fdiv_rn(__fmul_rn(g, __ldg(p.xs + my_tok)), 127.0f);
       }
       uint4 res[4];
       float bias = 0.f;
@@ -352,6 +352,20 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
       if (tile + npairs >= n_tiles) griddep_launch_dependents();   // the last tile's MMAs are done
       tc_fence_after();
       // chunk cc + 1 is read from TMEM while chunk cc is converted and stored
+      if constexpr (EPI) {
+#pragma unroll 1
+        for (int cc = 0; cc < nch; ++cc) {
+          const int c = c_first + cc;
+          const int tk = tok0 + 32 * c + lane;
+          const float sc_next = tk < p.T ? __fdiv_rn(__fmul_rn(g, __ldg(p.xs + tk)), 127.0f) : 0.f;
+          epi_chunk(ep, eo, et, tmem + lane_base + (uint32_t)(b * C::BN + 32 * c), sc_next, bias, row_w, tok0 + 32 * c,
+                    p.T, cc + 1 < nch ? tok0 + 32 * (c + 1) : -1, lane, res);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[b]);
+        continue;
+      }
       uint32_t ra[32], rb[32];
       tmem_ld32_issue(tmem + lane_base + (uint32_t)(b * C::BN + 32 * c_first), ra);
 #pragma unroll
@@ -362,10 +376,7 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
         uint32_t(&rn)[32] = (cc & 1) ? ra : rb;
         tmem_ld_wait(r);
         if (cc + 1 < nch) tmem_ld32_issue(tmem + lane_base + (uint32_t)(b * C::BN + 32 * (c + 1)), rn);
-        if constexpr (EPI) {
-          epi_chunk(ep, eo, et, r, scq[cc], bias, row_w, tok0 + 32 * c, p.T, cc + 1 < nch ? tok0 + 32 * (c + 1) : -1,
-                    lane, res);
-        } else if (!ACC && y_tma) {
+        if (!ACC && y_tma) {
           uint16_t* buf = wbuf + (nstore & 1) * 1024;
           if (lane == 0) tma_store_wait_read1();
           __syncwarp();

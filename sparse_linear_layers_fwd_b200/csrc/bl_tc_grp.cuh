@@ -8,7 +8,7 @@
 //
 // A persistent CTA per SM walks the tiles of the work list (grp.cuh): 128
 // output features x up to 160 rows of one expert, an expert's rows split into
-// equal tiles (a multiple of 16 rows each, the MMA's N). The packed weights
+// equal tiles (of 32-row chunks; the MMA's N is a multiple of 16). The packed weights
 // are read once per tile and expanded on the way to the MMA, since an expert
 // sees few rows: expanding them in memory first would cost as much as the
 // product itself at 500 rows.
@@ -25,7 +25,8 @@
 //   warps 4-15  producers: three groups of four warps, one for each stage of
 //               the ring; a thread expands its feature's 256 positions
 //               (bl_gemv.cuh's expansion), 32 registers per tcgen05.st;
-//   warps 16-19 epilogue (epi_tile.cuh).
+//   warps 16-23 epilogue (epi_tile.cuh), two per TMEM lane quadrant, the
+//               first taking the first half of a tile's 32-row chunks.
 // The loops of the MMA and TMA warps are run by whole warps and only the
 // instructions themselves by one elected lane: addresses and descriptors then
 // live in uniform registers, and eight MMAs are issued in 190 cycles instead
@@ -60,10 +61,11 @@ constexpr uint32_t kTgACol = 2 * kTgBN;        // A slots after the accumulators
 static_assert(kTgACol + 64 * kTgStages <= kTcTmemCols, "accumulators and A slots fit in TMEM");
 static_assert(kTgSub % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
 constexpr int kTgPackedBytes = kTgBM * (64 + 32);   // packed rows of a stage
-constexpr int kTgThreads = 640;
+constexpr int kTgThreads = 768;
 constexpr int kTgEpiWarp = 16;                 // first epilogue warp
 constexpr int kTgSelCopies = 4;
-constexpr int kTgYBuf = (kTcEpilogue / 32) * (4096 + 128);
+constexpr int kTgEpiWarps = 8;
+constexpr int kTgYBuf = kTgEpiWarps * (4096 + 128);
 constexpr int kTgBars = 4 * kTgStages + 4;
 constexpr int kTgList = 256;                   // tiles of a CTA whose place is worked out ahead
 constexpr uint32_t kTgIdesc0 = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTgBM >> 4) << 24);
@@ -98,7 +100,7 @@ SBN_DEVFN TgTile tg_tile(const int* off, const int* first, const GrpParams& g, i
   const int local = tile - first[t.e];
   const int lo = off[t.e], hi = off[t.e + 1], n = hi - lo;
   const int parts = (n + bn - 1) / bn;
-  const int size = ((n + parts - 1) / parts + step - 1) / step * step;
+  const int size = ((n + parts - 1) / parts + 31) / 32 * 32;   // whole chunks of the epilogue
   const int tt = local / row_tiles;
   t.row0 = (local - tt * row_tiles) * bm;
   t.tok0 = lo + tt * size;
@@ -192,7 +194,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kTcEpilogue / 32);
+      mbar_init(&acc_empty[b], kTgEpiWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -351,25 +353,22 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       it = end;
       for (; mine < end; mine += kTgStages, ph ^= 1u) {
         if (!mbar_wait(&p_full[s], ph)) { ok = false; break; }
-        uint2 cv[2 * CB];
-        uint4 mv[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-#pragma unroll
-        for (int j = 0; j < 2 * CB; ++j) cv[j] = cp[j];
-        if (!DENSE) {
-          mv[0] = mp[0];
-          mv[1] = mp[1];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_empty[s]);
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 2; ++j) {
           uint32_t cw[2][CB];
 #pragma unroll
-          for (int h = 0; h < 2 * CB; ++h) {
-            const uint2 c2 = cv[(2 * CB * j + h) / 2];
-            cw[h / CB][h % CB] = ((2 * CB * j + h) & 1) ? c2.y : c2.x;
+          for (int h = 0; h < CB; ++h) {
+            const uint2 c2 = cp[CB * j + h];
+            cw[2 * h / CB][2 * h % CB] = c2.x;
+            cw[(2 * h + 1) / CB][(2 * h + 1) % CB] = c2.y;
           }
-          const uint32_t m0[2] = {mv[j].x, mv[j].y}, m1[2] = {mv[j].z, mv[j].w};
+          uint4 mv = make_uint4(0u, 0u, 0u, 0u);
+          if (!DENSE) mv = mp[j];
+          if (j == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_empty[s]);
+          }
+          const uint32_t m0[2] = {mv.x, mv.y}, m1[2] = {mv.z, mv.w};
           uint32_t w[32];
           tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
           tg_expand64<MM, CB, DENSE>(cw[1], m1, sel, w + 16);
@@ -388,9 +387,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   } else if (warp >= kTgEpiWarp) {
     // ---- epilogue ----
     const int q = warp & 3;
+    const bool second = warp >= kTgEpiWarp + 4;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     EpiTile et{reinterpret_cast<uint16_t*>(ybuf + (size_t)(warp - kTgEpiWarp) * 4096),
-               reinterpret_cast<float*>(ybuf + (kTcEpilogue / 32) * 4096) + 32 * (warp - kTgEpiWarp), 0};
+               reinterpret_cast<float*>(ybuf + kTgEpiWarps * 4096) + 32 * (warp - kTgEpiWarp), 0};
     const EpiOut out{&tmap_y, &tmap_z, p.y, p.N, p.grp.rows, p.aligned != 0};
     for (int k = 0; k < count; ++k) {
       const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
@@ -400,27 +400,25 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       const float gm = __ldg(p.gamma + t.e);
       const float bias = (p.ep.bias && row_w + lane < p.N) ? __ldg(p.ep.bias + (size_t)t.e * p.N + row_w + lane) : 0.f;
       const int chunks = (t.tok_end - t.tok0 + 31) / 32;
+      const int c_first = second ? (chunks + 1) / 2 : 0, c_end = second ? chunks : (chunks + 1) / 2;
+      const int tok_w = t.tok0 + 32 * c_first;
       uint4 res[4];
-      epi_load_residual(p.ep, out, row_w, t.tok0, t.tok_end, lane, res);
-      float xs_n = t.tok0 + lane < t.tok_end ? __ldg(p.xs + t.tok0 + lane) : 0.f;
+      epi_load_residual(p.ep, out, row_w, tok_w, t.tok_end, lane, res);
+      float xs_n = tok_w + lane < t.tok_end ? __ldg(p.xs + tok_w + lane) : 0.f;
       if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
+      for (int c = c_first; c < c_end; ++c) {
         const int tok = t.tok0 + 32 * c;
-        uint32_t r[32];
-        tmem_ld32_issue(tmem + lane_base + (uint32_t)(b * kTgBN + 32 * c), r);
         const float sc = __fdiv_rn(__fmul_rn(gm, xs_n), 127.0f);
         xs_n = tok + 32 + lane < t.tok_end ? __ldg(p.xs + tok + 32 + lane) : 0.f;
-        tmem_ld_wait(r);
-        if (c + 1 == chunks) {   // the accumulator is in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
-        }
-        epi_chunk(p.ep, out, et, r, sc, bias, row_w, tok, t.tok_end, c + 1 < chunks ? tok + 32 : -1, lane, res);
+        epi_chunk(p.ep, out, et, tmem + lane_base + (uint32_t)(b * kTgBN + 32 * c), sc, bias, row_w, tok, t.tok_end,
+                  c + 1 < c_end ? tok + 32 : -1, lane, res);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
     }
     if (lane == 0) tma_store_wait_all();
     griddep_launch_dependents();

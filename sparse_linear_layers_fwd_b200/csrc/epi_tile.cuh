@@ -56,70 +56,95 @@ SBN_DEVFN void epi_store_rows(uint16_t* dst, const uint16_t* tile, int N, int ro
   }
 }
 
-// One chunk. r: accumulators of feature row_w + lane and tokens tok .. tok +
-// 31; sc: gamma s / 127 of token tok + lane; bias: of the lane's feature. res
-// is this chunk's residual and is reloaded for the next one (next_tok < 0: none).
-SBN_DEVFN void epi_chunk(const EpiParams& ep, const EpiOut& o, EpiTile& t, const uint32_t (&r)[32], float sc, float bias,
+// 16 columns of this warp's 32 lanes. Load and wait in one statement: between
+// the two the registers must not be touched, and a compiler may well copy
+// them there when they live across a loop's edge.
+SBN_DEVFN void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// One chunk, sixteen tokens at a time in a rolled loop: unrolled over all 32,
+// its code and the producers' kept evicting each other from the instruction
+// cache. taddr: the chunk's accumulators (feature row_w + lane, tokens tok ..
+// tok + 31); sc: gamma s / 127 of token tok + lane; bias: of the lane's
+// feature. res is this chunk's residual and is reloaded for the next one
+// (next_tok < 0: none).
+SBN_DEVFN void epi_chunk(const EpiParams& ep, const EpiOut& o, EpiTile& t, uint32_t taddr, float sc, float bias,
                          int row_w, int tok, int tok_end, int next_tok, int lane, uint4 (&res)[4]) {
-  // the tokens' factors by 16-byte broadcast reads (a shuffle per element
-  // cost as much as the rest of a plain epilogue)
-  float v[32];
-  t.sc[lane] = sc;
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 f = reinterpret_cast<const float4*>(t.sc)[j];
-    v[4 * j] = __fmaf_rn((float)(int32_t)r[4 * j], f.x, bias);
-    v[4 * j + 1] = __fmaf_rn((float)(int32_t)r[4 * j + 1], f.y, bias);
-    v[4 * j + 2] = __fmaf_rn((float)(int32_t)r[4 * j + 2], f.z, bias);
-    v[4 * j + 3] = __fmaf_rn((float)(int32_t)r[4 * j + 3], f.w, bias);
-  }
-  __syncwarp();
   const int row = row_w + lane;
-  if (!o.aligned) {
-    if (ep.z) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (row < o.N && tok + j < tok_end) ep.z[(size_t)(tok + j) * o.N + row] = f32_to_bf16_bits(v[j]);
-    }
-    act_all(ep.act, v);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (row < o.N && tok + j < tok_end) {
-        const size_t at = (size_t)(tok + j) * o.N + row;
-        if (ep.residual) v[j] = __fadd_rn(v[j], bf16_bits_to_float(ep.residual[at]));
-        o.y[at] = f32_to_bf16_bits(v[j]);
-      }
-    }
-    return;
-  }
   const bool whole = tok + 32 <= tok_end || tok_end == o.rows;
   const bool inside = row_w < o.N && tok < tok_end;
   uint16_t* zb = t.buf;
   uint16_t* yb = t.buf + (ep.z ? 1024 : (t.nstore & 1) * 1024);
-  if (lane == 0) {
-    if (ep.z) tma_store_wait_read0();
-    else tma_store_wait_read1();
+  __syncwarp();   // the previous chunk's reads of the factors are done
+  t.sc[lane] = sc;
+  if (o.aligned) {
+    if (lane == 0) {
+      if (ep.z) tma_store_wait_read0();
+      else tma_store_wait_read1();
+    }
+    __syncwarp();
+    if (ep.residual) {
+      uint4* d = reinterpret_cast<uint4*>(yb + lane * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = res[i];
+      if (next_tok >= 0) epi_load_residual(ep, o, row_w, next_tok, tok_end, lane, res);
+    }
   }
   __syncwarp();
-  if (ep.residual) {
-    uint4* d = reinterpret_cast<uint4*>(yb + lane * 32);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[16];
+    tmem_ld16(taddr + 16u * (uint32_t)h, r);
+    // the tokens' factors by 16-byte broadcast reads (a shuffle per element
+    // cost as much as the rest of a plain epilogue)
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = res[i];
-    if (next_tok >= 0) epi_load_residual(ep, o, row_w, next_tok, tok_end, lane, res);
-    __syncwarp();
+    for (int j = 0; j < 4; ++j) {
+      const float4 f = reinterpret_cast<const float4*>(t.sc)[4 * h + j];
+      v[4 * j] = __fmaf_rn((float)(int32_t)r[4 * j], f.x, bias);
+      v[4 * j + 1] = __fmaf_rn((float)(int32_t)r[4 * j + 1], f.y, bias);
+      v[4 * j + 2] = __fmaf_rn((float)(int32_t)r[4 * j + 2], f.z, bias);
+      v[4 * j + 3] = __fmaf_rn((float)(int32_t)r[4 * j + 3], f.w, bias);
+    }
+    if (o.aligned) {
+      const int at = 512 * h + lane;
+      if (ep.z) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) zb[at + 32 * j] = f32_to_bf16_bits(v[j]);
+      }
+      act_all(ep.act, v);
+      if (ep.residual) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], bf16_bits_to_float(yb[at + 32 * j]));
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) yb[at + 32 * j] = f32_to_bf16_bits(v[j]);
+    } else {
+      const int tk = tok + 16 * h;
+      const size_t at = (size_t)tk * o.N + row;
+      if (ep.z) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (row < o.N && tk + j < tok_end) ep.z[at + (size_t)j * o.N] = f32_to_bf16_bits(v[j]);
+      }
+      act_all(ep.act, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (row < o.N && tk + j < tok_end) {
+          if (ep.residual) v[j] = __fadd_rn(v[j], bf16_bits_to_float(ep.residual[at + (size_t)j * o.N]));
+          o.y[at + (size_t)j * o.N] = f32_to_bf16_bits(v[j]);
+        }
+      }
+    }
   }
-  if (ep.z) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) zb[j * 32 + lane] = f32_to_bf16_bits(v[j]);
-  }
-  act_all(ep.act, v);
-  if (ep.residual) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __fadd_rn(v[j], bf16_bits_to_float(yb[j * 32 + lane]));
-  }
-#pragma unroll
-  for (int j = 0; j < 32; ++j) yb[j * 32 + lane] = f32_to_bf16_bits(v[j]);
+  if (!o.aligned) return;
   if (whole) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   __syncwarp();
   if (!inside) return;
