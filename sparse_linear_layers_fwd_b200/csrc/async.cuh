@@ -59,6 +59,13 @@ SBN_DEVFN bool mbar_test(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// True in one lane of the warp (all lanes must call it).
+SBN_DEVFN bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0u;
+}
+
 // Bulk copy (no tensor map) of `bytes` (a multiple of 16, both addresses
 // 16-byte aligned) from global to this CTA's shared memory, completing
 // `bytes` transactions on `bar`.

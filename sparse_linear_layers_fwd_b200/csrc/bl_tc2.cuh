@@ -34,7 +34,7 @@
 //   warp 0   TMA into the CTA's own shared memory; the completions of both
 //            CTAs count on the leader CTA's `full` barrier, for which the
 //            leader's producer declares the pair's bytes;
-//   warp 1   TMEM allocation for the pair; in the leader, the MMA thread.
+//   warp 1   TMEM allocation for the pair; in the leader, the MMA warp.
 //            Its commits arrive on the `empty` and `acc_full` barriers of
 //            both CTAs (multicast commit);
 //   warp 2   in the peer CTA, the relay: once its eight epilogue warps have
@@ -209,19 +209,20 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
   if (warp == 0) {
     // ---- TMA producer (both CTAs): every box of a stage is loaded, the
     // second block of a half stage as zeros, so each stage is STAGE bytes ----
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = pair; tile < n_tiles && ok; tile += npairs) {
-        const int tok0 = (tile / row_pairs) * C::BN + (int)rank * C::HALF;
-        const int row0 = (tile % row_pairs) * 256 + (int)rank * 128;
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          const int s = it % C::STAGES;
-          const uint32_t ph = (it / C::STAGES) & 1u;
-          if (!mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+    const bool lead = elect_one();
+    const uint32_t full0 = map_to_rank(smem_u32(full), 0);   // the leader's barriers
+    int s = 0;
+    uint32_t ph = 1u;
+    bool ok = true;
+    for (int tile = pair; tile < n_tiles && ok; tile += npairs) {
+      const int tok0 = (tile / row_pairs) * C::BN + (int)rank * C::HALF;
+      const int row0 = (tile % row_pairs) * 256 + (int)rank * 128;
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        const uint32_t fb = full0 + 8u * (uint32_t)s;
+        uint8_t* st = smem + (size_t)s * C::STAGE;
+        if (lead) {
           if (leader) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)C::STAGE);
-          const uint32_t fb = map_to_rank(smem_u32(&full[s]), 0);
-          uint8_t* st = smem + (size_t)s * C::STAGE;
           if (SPARSE) {
             tma_load_2d_pair(st, &tmap_w, ks * 128, row0, fb);
           } else {
@@ -234,16 +235,17 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
             if (SPARSE) tma_load_2d_pair(st + C::ABYTES + C::BBYTES + j * C::ESUB, &tmap_e, ks * 32 + j * 16, row0, fb);
           }
         }
+        __syncwarp();
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
       }
     }
   } else if (warp == 1) {
-    // ---- MMA issuer (leader CTA) ----
-    // The tensor core takes few MMAs ahead, so the thread spends most of a
-    // stage blocked on issue, and what it does between two stages leaves the
-    // pipe idle: there it only commits, probes the next `full` barrier (the
-    // bounded wait runs only if the data is late) and picks the stage's
-    // precomputed descriptors.
-    if (leader && lane == 0) {
+    // ---- MMA issuer (leader CTA): the whole warp runs the loop, so that
+    // descriptors and addresses stay in uniform registers, and one elected lane
+    // issues. With one lane running the loop, eight MMAs took 840 cycles to
+    // issue instead of 190, and the thread was the kernel's bound ----
+    if (leader) {
+      const bool lead = elect_one();
       // descriptors of stage 0; stage s adds s * STAGE bytes to the start
       // address field (16-byte units)
       const uint32_t a0 = smem_u32(smem);
@@ -251,43 +253,48 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
       const uint64_t bdesc0 = sw128_kmajor_desc(a0 + C::ABYTES);
       const uint64_t edesc0 = meta_stage_desc(a0 + C::ABYTES + C::BBYTES);
       static_assert(!SPARSE || C::ESUB == 2048, "the stage copy takes the two metadata blocks 2 KB apart");
-      int it = 0, jt = 0;
+      int s = 0, jt = 0;
+      uint32_t ph = 0u;
       bool ok = true;
       for (int tile = pair; tile < n_tiles && ok; tile += npairs, ++jt) {
         const int b = jt & 1;
         const uint32_t pa = ((jt >> 1) & 1u) ^ 1u;
         if (!mbar_wait(&acc_empty[b], pa) || !mbar_wait(&acc_peer[b], pa)) break;
-        tc_fence_after();
         const uint32_t d_tmem = tmem + (uint32_t)(b * C::BN);
-        int s = it % C::STAGES;
-        uint32_t ph = (it / C::STAGES) & 1u;
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          if (!mbar_test(&full[s], ph) && !mbar_wait(&full[s], ph)) { ok = false; break; }
+        for (int ks = 0; ks < nst; ++ks) {
+          if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+          tc_fence_after();
           const uint32_t e_tmem = tmem + C::ECOL + 8u * (uint32_t)s;
+          const uint64_t so = (uint64_t)(s * (C::STAGE / 16));
           const int nsub = (2 * ks + 1 < nkb) ? 2 : 1;
-          // both blocks' metadata (a half stage's second block is zeros)
-          if (SPARSE) tc_cp_meta_stage_pair(e_tmem, edesc0 + (uint64_t)(s * (C::STAGE / 16)));
-          for (int j = 0; j < nsub; ++j) {
-            // A: sparse, one 128-byte swizzled row of kept values per 256
-            // positions (block j at +64 bytes, MMA k at +32 bytes); dense,
-            // one swizzled tile per block (16 KB apart, MMA k at +32 bytes).
-            // Descriptor addresses count 16-byte units.
-            const uint64_t so = (uint64_t)(s * (C::STAGE / 16));
-            const uint64_t adesc = adesc0 + so + (uint64_t)(SPARSE ? 4 * j : j * (128 * 128 / 16));
-            const uint64_t bdesc = bdesc0 + so + (uint64_t)(j * (C::BSUB / 16));
+          if (lead) {
+            // both blocks' metadata (a half stage's second block is zeros)
+            if (SPARSE) tc_cp_meta_stage_pair(e_tmem, edesc0 + so);
 #pragma unroll
-            for (int k = 0; k < C::MMAS; ++k) {
-              // B advances 64 bytes per sparse MMA (64 positions), 32 per
-              // dense one; A 32 bytes either way; metadata two columns
-              tc_mma_pair<SPARSE, C::IDESC>(d_tmem, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)((SPARSE ? 4 : 2) * k),
-                                  e_tmem + 4u * (uint32_t)j + 2u * (uint32_t)k,
-                                  (ks > 0 || j > 0 || k > 0) ? 1u : 0u);
+            for (int j = 0; j < 2; ++j) {
+              if (j == 1 && nsub == 1) break;
+              // A: sparse, one 128-byte swizzled row of kept values per 256
+              // positions (block j at +64 bytes, MMA k at +32 bytes); dense,
+              // one swizzled tile per block (16 KB apart, MMA k at +32 bytes).
+              // Descriptor addresses count 16-byte units.
+              const uint64_t adesc = adesc0 + so + (uint64_t)(SPARSE ? 4 * j : j * (128 * 128 / 16));
+              const uint64_t bdesc = bdesc0 + so + (uint64_t)(j * (C::BSUB / 16));
+#pragma unroll
+              for (int k = 0; k < C::MMAS; ++k) {
+                // B advances 64 bytes per sparse MMA (64 positions), 32 per
+                // dense one; A 32 bytes either way; metadata two columns
+                tc_mma_pair<SPARSE, C::IDESC>(d_tmem, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)((SPARSE ? 4 : 2) * k),
+                                              e_tmem + 4u * (uint32_t)j + 2u * (uint32_t)k,
+                                              (ks > 0 || j > 0 || k > 0) ? 1u : 0u);
+              }
             }
+            tc_commit_pair(&empty[s]);
           }
-          tc_commit_pair(&empty[s]);
+          __syncwarp();
           if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
-        tc_commit_pair(&acc_full[b]);
+        if (lead) tc_commit_pair(&acc_full[b]);
+        __syncwarp();
       }
       // the accumulators may be freed only after the last MMAs completed
       // (matters on the abort path only)

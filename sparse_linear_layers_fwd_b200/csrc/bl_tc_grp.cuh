@@ -110,11 +110,6 @@ SBN_DEVFN TgTile tg_tile(const int* off, const int* first, const GrpParams& g, i
   return t;
 }
 
-SBN_DEVFN bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0u;
-}
 // A from tensor memory, B from shared memory.
 SBN_DEVFN void tc_mma_i8_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
