@@ -19,10 +19,18 @@
 // Rows of the next expert in a tile are multiplied too (rows are
 // independent) and not stored.
 //
-// dW: tiles of 128 features x 256 positions of one expert, 64 rows per
-// stage. Xq is exact in bf16; a = fp32(dY s / 127) is split into a_hi =
-// bf16(a) and a_lo = bf16(a - a_hi) (|a - a_hi - a_lo| <= 2^-18 |a|), two MMAs
-// per step. Producers write all operands (MN-major), zeros behind the range.
+// dW in two kernels. bwd_dw_prep_kernel lays the operands out once in the
+// caller's workspace, as fp16, every expert's rows padded with zeros to a
+// multiple of 64: Xq (exact) and a = dY s / 127 times a power of two per
+// (expert, feature) that brings the largest |a| of the feature just below
+// 2^15. fp16 keeps 11 bits of an a within 2^-29 of that largest, so each
+// product is within 2^-11 of itself, an eighth of the bf16 result's own
+// rounding; bf16 would keep 8 bits, and two bf16 parts (as in bwd_tc.cuh) take
+// twice the MMAs. bwd_dw_grp_kernel then is a plain TMA-fed product over
+// tiles of 128 features x 256 positions, both operands MN-major (features and
+// positions are contiguous in a row): 1 KB atoms of 8 rows x 64 columns.
+// Converting in the product's own producer warps instead, for every tile
+// again, took six times as long as its MMAs.
 #pragma once
 
 #include <cuda.h>
@@ -43,9 +51,6 @@ constexpr int kGxSelCopies = kTgSelCopies;
 __host__ __device__ inline size_t gx_smem_bytes(int experts) {
   return 1024 + (size_t)kBxStages * kBxStageBytes + 256 * 8 * kGxSelCopies + (2 * kBxStages + 4) * 8 + 16 +
          2 * 4 * (size_t)(experts + 1);
-}
-__host__ __device__ inline size_t gw_smem_bytes(int experts) {
-  return kBwSmemBytes + 2 * 4 * (size_t)(experts + 1);
 }
 
 struct GxParams {
@@ -262,32 +267,203 @@ struct GwParams {
   uint16_t* dw;     // [E, N, K]
   GrpParams grp;
   int K, N;
+  // workspace: fp16 [padded rows, N] and [padded rows, K], and the factor
+  // that undoes the scaling of a, [E, N]
+  uint16_t* a16;
+  uint16_t* x16;
+  float* scale;
+  int cluster;      // CTAs per (expert, 64 columns) in the preparation
+  int a_ctas;       // its CTAs that scale dY; the others convert Xq
 };
 
-static __global__ void __launch_bounds__(kTcThreads, 1) bwd_dw_grp_kernel(const GwParams p) {
+// Rows of the padded operands: every expert with rows ends a block of 64.
+__host__ __device__ inline long long gw_padded_rows(int rows, int experts) {
+  return ((long long)rows + 63ll * (experts < rows ? experts : rows)) / 64 * 64;
+}
+
+constexpr int kGpThreads = 256;
+constexpr int kGpCols = 64;
+constexpr int kGpLanes = kGpThreads / 8;   // row lanes: 8 threads x 8 columns make a row of 64
+
+// CTAs [0, a_ctas): cluster c of (expert, column block), blockIdx = ((expert *
+// blocks) + block) * cluster + rank: the features' largest |a| over the
+// expert's rows, then a scaled. The other CTAs: Xq to fp16, one row (of a
+// block of 64) per warp.
+static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const GwParams p) {
+  extern __shared__ int s_list[];
+  __shared__ uint32_t s_max[kGpCols];
+  __shared__ float s_mult[kGpCols];
+  int* s_off = s_list;
+  int* s_first = s_list + p.grp.experts + 1;   // blocks of 64 rows before an expert
+  const int tid = threadIdx.x;
+  griddep_wait();
+  if (tid < 32) grp_build(p.grp, 64, 1, 0, s_off, s_first);
+  if (tid < kGpCols) s_max[tid] = 0u;
+  __syncthreads();
+  const int blocks = (p.N + kGpCols - 1) / kGpCols;
+  if ((int)blockIdx.x < p.a_ctas) {
+    const int rank = (int)blockIdx.x % p.cluster, eb = (int)blockIdx.x / p.cluster;
+    const int e = eb / blocks, c0 = (eb - e * blocks) * kGpCols;
+    const int lo = s_off[e], hi = s_off[e + 1];
+    const int col = c0 + 8 * (tid & 7), lane_r = tid >> 3;
+    const bool in = col < p.N;   // N is a multiple of 8
+    const int step = p.cluster * kGpLanes;
+    uint32_t top[8] = {};
+    for (int r0 = lo + rank * kGpLanes + lane_r; r0 < hi; r0 += 4 * step) {
+      uint4 v[4];
+      float sc[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + u * step;
+        const bool ok = in && r < hi;
+        v[u] = ok ? __ldg(reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col)) : make_uint4(0u, 0u, 0u, 0u);
+        sc[u] = ok ? __fdiv_rn(__ldg(p.xs + r), 127.0f) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          top[2 * j] = max(top[2 * j], __float_as_uint(fabsf(__fmul_rn(__uint_as_float(w[j] << 16), sc[u]))));
+          top[2 * j + 1] = max(top[2 * j + 1], __float_as_uint(fabsf(__fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), sc[u]))));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // lanes 8 apart share the columns
+      top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+      top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+      if ((tid & 31) < 8) atomicMax(&s_max[8 * (tid & 7) + j], top[j]);
+    }
+    __syncthreads();
+    if (p.cluster > 1) cluster_sync_all();
+    if (tid < kGpCols) {
+      uint32_t m = s_max[tid];
+      for (int c = 0; c < p.cluster; ++c) {
+        if (c == rank) continue;
+        uint32_t o;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(o) : "r"(map_to_rank(smem_u32(&s_max[tid]), (uint32_t)c)));
+        m = max(m, o);
+      }
+      const int ex = min(max((int)(m >> 23) - 127, -100), 126);
+      s_mult[tid] = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+      if (rank == 0 && c0 + tid < p.N)
+        p.scale[(size_t)e * p.N + c0 + tid] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+    }
+    if (p.cluster > 1) cluster_sync_all();   // no CTA leaves while its maxima are read
+    __syncthreads();
+    const int pad_hi = lo + (hi - lo + 63) / 64 * 64;
+    uint16_t* dst = p.a16 + ((size_t)s_first[e] * 64) * p.N + col;
+    float mult[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mult[j] = s_mult[8 * (tid & 7) + j];
+    for (int r0 = lo + rank * kGpLanes + lane_r; r0 < pad_hi; r0 += 4 * step) {
+      uint4 v[4];
+      float sc[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + u * step;
+        const bool ok = in && r < hi;
+        v[u] = ok ? __ldg(reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col)) : make_uint4(0u, 0u, 0u, 0u);
+        sc[u] = ok ? __fdiv_rn(__ldg(p.xs + r), 127.0f) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + u * step;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a0 = __fmul_rn(__fmul_rn(__uint_as_float(w[j] << 16), sc[u]), mult[2 * j]);
+          const float a1 = __fmul_rn(__fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), sc[u]), mult[2 * j + 1]);
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(a1), "f"(a0));
+        }
+        if (in && r < pad_hi) *reinterpret_cast<uint4*>(dst + (size_t)(r - lo) * p.N) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+    griddep_launch_dependents();
+    return;
+  }
+  // ---- Xq: warp w of these CTAs takes padded rows w, w + warps, ... ----
+  const int n_rows = s_first[p.grp.experts] * 64;
+  const int warps = ((int)gridDim.x - p.a_ctas) * (kGpThreads / 32);
+  const int lane = tid & 31;
+  for (int pr = ((int)blockIdx.x - p.a_ctas) * (kGpThreads / 32) + (tid >> 5); pr < n_rows; pr += warps) {
+    const int e = grp_find(s_first, p.grp.experts, pr >> 6);
+    const int r = s_off[e] + pr - s_first[e] * 64;
+    const bool ok = r < s_off[e + 1];
+    const uint4* src = reinterpret_cast<const uint4*>(p.xq + (size_t)r * p.K);
+    uint4* d = reinterpret_cast<uint4*>(p.x16 + (size_t)pr * p.K);
+    for (int c = lane; c < p.K / 16; c += 32) {
+      const uint4 v = ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t h[8];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // bytes b + 128 as the low mantissa bits of 1024: exact, then - 1152
+        const uint32_t u = w[j] ^ 0x80808080u;
+        const uint32_t lo2 = __byte_perm(u, 0x64646464u, 0x4140u), hi2 = __byte_perm(u, 0x64646464u, 0x4342u);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * j]) : "r"(lo2), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * j + 1]) : "r"(hi2), "r"(0x64806480u));
+      }
+      d[2 * c] = make_uint4(h[0], h[1], h[2], h[3]);
+      d[2 * c + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+  }
+  griddep_launch_dependents();
+}
+
+constexpr int kGwBM = 128;                       // features per tile (MMA M)
+constexpr int kGwBN = 256;                       // positions per tile (MMA N)
+constexpr int kGwBK = 64;                        // rows per stage
+constexpr int kGwStages = 4;
+constexpr int kGwABytes = kGwBM * kGwBK * 2;     // 16 KB
+constexpr int kGwStageBytes = kGwABytes + kGwBN * kGwBK * 2;
+constexpr int kGwThreads = 384;                  // TMA, MMA, list, -, eight epilogue warps
+// instruction descriptor: f32 accumulate, fp16 A and B, both MN-major
+constexpr uint32_t kGwIdesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(kGwBN >> 3) << 17) |
+                              ((uint32_t)(kGwBM >> 4) << 24);
+
+__host__ __device__ inline size_t gw_smem_bytes(int experts) {
+  return 1024 + (size_t)kGwStages * kGwStageBytes + (2 * kGwStages + 4) * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
+}
+
+SBN_DEVFN void tc_mma_f16_gw(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(kGwIdesc), "r"(accumulate), "r"(0u)
+      : "memory");
+}
+
+// tmap_a, tmap_x: the fp16 operands, boxes of 64 columns x 64 rows (128-byte swizzle).
+static __global__ void __launch_bounds__(kGwThreads, 1)
+bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_x,
+                  const GwParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kBwStages * kBwStageBytes);
-  uint64_t* empty = full + kBwStages;
-  uint64_t* acc_full = empty + kBwStages;   // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kGwStages * kGwStageBytes);
+  uint64_t* empty = full + kGwStages;
+  uint64_t* acc_full = empty + kGwStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
   int* s_off = reinterpret_cast<int*>(s_tmem + 4);
   int* s_first = s_off + p.grp.experts + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int col_tiles = (p.K + kBwBN - 1) / kBwBN;
-  const int per_expert = col_tiles * ((p.N + kBwBM - 1) / kBwBM);
+  const int col_tiles = (p.K + kGwBN - 1) / kGwBN;
+  const int per_expert = col_tiles * ((p.N + kGwBM - 1) / kGwBM);
   const int n_tiles = p.grp.experts * per_expert, grid = (int)gridDim.x;
 
   if (tid == 0) {
-    for (int s = 0; s < kBwStages; ++s) {
-      mbar_init(&full[s], kTcProducers / 32);
+    for (int s = 0; s < kGwStages; ++s) {
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kTcEpilogue / 32);
+      mbar_init(&acc_empty[b], 8);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -298,122 +474,102 @@ static __global__ void __launch_bounds__(kTcThreads, 1) bwd_dw_grp_kernel(const 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   griddep_wait();
-  if (warp == 2) grp_build(p.grp, 1, 0, 0, s_off, s_first);
+  if (warp == 2) grp_build(p.grp, kGwBK, 1, 0, s_off, s_first);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   int used = 0;
 
-  if (warp == 1) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-        const int e = tile / per_expert;
-        const int nst = (s_off[e + 1] - s_off[e] + kBwBK - 1) / kBwBK;
-        if (nst == 0) continue;
-        const int b = used & 1;
-        if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)(b * kBwBN);
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          const int s = it % kBwStages;
-          if (!mbar_wait(&full[s], (it / kBwStages) & 1u)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t base = smem_u32(smem + (size_t)s * kBwStageBytes);
-          const uint64_t ahi = sw128_mnmajor_desc(base, 1024u, 2048u);
-          const uint64_t alo = sw128_mnmajor_desc(base + kBwAPlane, 1024u, 2048u);
-          const uint64_t bd = sw128_mnmajor_desc(base + 2 * kBwAPlane, 1024u, 4096u);
-#pragma unroll
-          for (int k = 0; k < kBwBK / 16; ++k) {
-            tc_mma_f16_mn(d_tmem, ahi + (uint64_t)(k * (4096 / 16)), bd + (uint64_t)(k * (8192 / 16)),
-                          (ks > 0 || k > 0) ? 1u : 0u);
-            tc_mma_f16_mn(d_tmem, alo + (uint64_t)(k * (4096 / 16)), bd + (uint64_t)(k * (8192 / 16)), 1u);
-          }
-          tc_commit(&empty[s]);
-        }
-        tc_commit(&acc_full[b]);
-        ++used;
-      }
-      for (int j = used - 2; j < used; ++j)
-        if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
-    }
-    __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
-    const int pi = tid - 128;
-    int it = 0;
+  if (warp == 0) {
+    const bool lead = elect_one();
+    int s = 0;
+    uint32_t ph = 1u;
     bool ok = true;
     for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
       const int e = tile / per_expert, local = tile - e * per_expert;
-      const int lo = s_off[e], hi = s_off[e + 1];
-      const int nst = (hi - lo + kBwBK - 1) / kBwBK;
-      const int o0 = (local / col_tiles) * kBwBM, k0 = (local % col_tiles) * kBwBN;
-      for (int ks = 0; ks < nst; ++ks, ++it) {
-        const int s = it % kBwStages;
-        int got = 1;
-        if (lane == 0) got = mbar_wait(&empty[s], ((it / kBwStages) & 1u) ^ 1u) ? 1 : 0;
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) { ok = false; break; }
-        uint8_t* st = smem + (size_t)s * kBwStageBytes;
+      const int b0 = s_first[e], nst = s_first[e + 1] - b0;
+      const int o0 = (local / col_tiles) * kGwBM, k0 = (local % col_tiles) * kGwBN;
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        uint8_t* st = smem + (size_t)s * kGwStageBytes;
+        const int row = __shfl_sync(0xffffffffu, (b0 + ks) * kGwBK, 0);
+        if (lead) {
+          // boxes past the last column are zeros
+          mbar_arrive_expect_tx(&full[s], (uint32_t)kGwStageBytes);
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const int i = pi + 256 * q4, tl = i >> 4, f8 = i & 15;
-          const int t = lo + ks * kBwBK + tl, r = tl & 7;
-          {   // A: row t, features 8 f8 ..
-            const int o = o0 + 8 * f8;
-            uint4 hi4 = make_uint4(0u, 0u, 0u, 0u), lo4 = hi4;
-            if (t < hi && o < p.N) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.dy + (size_t)t * p.N + o));
-              scale_split8(v, __fdiv_rn(__ldg(p.xs + t), 127.0f), hi4, lo4);
-            }
-            const size_t off = (size_t)(tl >> 3) * 2048 + (size_t)(f8 >> 3) * 1024 + (size_t)r * 128 + (((f8 & 7) ^ r) << 4);
-            *reinterpret_cast<uint4*>(st + off) = hi4;
-            *reinterpret_cast<uint4*>(st + kBwAPlane + off) = lo4;
-          }
-          {   // B: row t, positions 16 u ..
-            const int u = f8, kk = k0 + 16 * u;
-            uint32_t h[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            if (t < hi && kk < p.K) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.xq + (size_t)t * p.K + kk));
-              s8x4_to_bf16x4_any(v.x, h[0], h[1]);
-              s8x4_to_bf16x4_any(v.y, h[2], h[3]);
-              s8x4_to_bf16x4_any(v.z, h[4], h[5]);
-              s8x4_to_bf16x4_any(v.w, h[6], h[7]);
-            }
-            const int c0 = 2 * (u & 3);
-            uint8_t* atom = st + 2 * kBwAPlane + (size_t)(tl >> 3) * 4096 + (size_t)(u >> 2) * 1024 + (size_t)r * 128;
-            *reinterpret_cast<uint4*>(atom + ((c0 ^ r) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(atom + (((c0 + 1) ^ r) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
+          for (int j = 0; j < kGwBM / 64; ++j) tma_load_2d(st + j * 8192, &tmap_a, o0 + 64 * j, row, &full[s]);
+#pragma unroll
+          for (int j = 0; j < kGwBN / 64; ++j) tma_load_2d(st + kGwABytes + j * 8192, &tmap_x, k0 + 64 * j, row, &full[s]);
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == kGwStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
     }
-  } else if (warp >= 12) {
-    const int q = warp & 3;
+  } else if (warp == 1) {
+    // ---- MMA issuer: the whole warp runs the loop, one elected lane issues ----
+    const bool lead = elect_one();
+    const uint32_t base = smem_u32(smem);
+    const uint64_t ad0 = sw128_mnmajor_desc(base, 8192u, 1024u), bd0 = sw128_mnmajor_desc(base + kGwABytes, 8192u, 1024u);
+    int s = 0;
+    uint32_t ph = 0u;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
+      const int e = tile / per_expert;
+      const int nst = s_first[e + 1] - s_first[e];
+      if (nst == 0) continue;
+      const int b = used & 1;
+      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      const uint32_t d_tmem = tmem + (uint32_t)(b * kGwBN);
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t so = (uint64_t)(s * (kGwStageBytes / 16));
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < kGwBK / 16; ++k)   // 16 rows: two 1 KB atom rows of each operand
+            tc_mma_f16_gw(d_tmem, ad0 + so + (uint64_t)(k * (2048 / 16)), bd0 + so + (uint64_t)(k * (2048 / 16)),
+                          (ks > 0 || k > 0) ? 1u : 0u);
+          tc_commit(&empty[s]);
+        }
+        __syncwarp();
+        if (++s == kGwStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (lead) tc_commit(&acc_full[b]);
+      __syncwarp();
+      ++used;
+    }
+    for (int j = used - 2; j < used; ++j)
+      if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- epilogue: lane = feature, 32 positions per TMEM load; the second
+    // warp of a lane quadrant takes the second half of the positions ----
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     for (int tile = blockIdx.x; tile < n_tiles; tile += grid) {
       const int e = tile / per_expert, local = tile - e * per_expert;
-      const bool any = s_off[e + 1] > s_off[e];
+      const bool any = s_first[e + 1] > s_first[e];
       const int b = used & 1;
-      const int o = (local / col_tiles) * kBwBM + 32 * q + lane, k0 = (local % col_tiles) * kBwBN;
+      const int o = (local / col_tiles) * kGwBM + 32 * q + lane, k0 = (local % col_tiles) * kGwBN;
+      const float sc = any && o < p.N ? __ldg(p.scale + (size_t)e * p.N + o) : 0.f;
       if (any) {
-        int got = 1;
-        if (lane == 0) got = mbar_wait(&acc_full[b], (used >> 1) & 1u) ? 1 : 0;
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) break;
+        if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
         ++used;
         tc_fence_after();
       }
       uint16_t* drow = p.dw + ((size_t)e * p.N + o) * p.K;
 #pragma unroll 1
-      for (int c = 0; c < kBwBN / 32; ++c) {
+      for (int c = 4 * half; c < 4 * half + 4; ++c) {
         uint32_t r[32];
         if (any) {
-          tmem_ld32(tmem + lane_base + (uint32_t)(b * kBwBN + 32 * c), r);
+          tmem_ld32(tmem + lane_base + (uint32_t)(b * kGwBN + 32 * c), r);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = 0u;
@@ -423,8 +579,8 @@ static __global__ void __launch_bounds__(kTcThreads, 1) bwd_dw_grp_kernel(const 
           uint32_t o16[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            o16[i] = (uint32_t)f32_to_bf16_bits(__uint_as_float(r[2 * i])) |
-                     ((uint32_t)f32_to_bf16_bits(__uint_as_float(r[2 * i + 1])) << 16);
+            o16[i] = (uint32_t)f32_to_bf16_bits(__fmul_rn(sc, __uint_as_float(r[2 * i]))) |
+                     ((uint32_t)f32_to_bf16_bits(__fmul_rn(sc, __uint_as_float(r[2 * i + 1]))) << 16);
           uint4* dst = reinterpret_cast<uint4*>(drow + kc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_uint4(o16[4 * i], o16[4 * i + 1], o16[4 * i + 2], o16[4 * i + 3]);

@@ -37,6 +37,18 @@ struct LaunchDx {
   }
 };
 
+// Workspace of dW: the fp16 operands over padded rows, and the scales.
+struct GwLayout {
+  long long rows;
+  size_t x16, scale, total;
+  GwLayout(int r, int e, int k, int n) {
+    rows = gw_padded_rows(r, e);
+    x16 = ((size_t)rows * n * 2 + 127) & ~(size_t)127;
+    scale = x16 + (((size_t)rows * k * 2 + 127) & ~(size_t)127);
+    total = scale + round_up16((size_t)e * n * 4);
+  }
+};
+
 sbn_status check_grad(int rows, const int32_t* offsets, int experts, int k, int n_out) {
   if (rows < 1 || n_out < 1 || k < 128 || (k % 128) != 0 || experts < 1 || experts > kGrpMaxExperts) return SBN_ERR_SHAPE;
   if (!prod_lt_2_31(rows, k) || !prod_lt_2_31(n_out, k) || !prod_lt_2_31(rows, n_out) ||
@@ -73,29 +85,63 @@ sbn_status sbn_bitlinear_grouped_grad_x(const void* dy_bf16, int32_t rows, const
                               reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t sbn_bitlinear_grouped_grad_w_workspace_bytes(int32_t rows, int32_t experts, int32_t k, int32_t n_out) {
+  if (check_grad(rows, nullptr, experts, k, n_out) != SBN_OK || n_out % 8 != 0) return 0;
+  const GwLayout l(rows, experts, k, n_out);
+  return l.total;
+}
+
 sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, const float* x_scale, int32_t rows,
                                         const int32_t* offsets, int32_t experts, int32_t k, int32_t n_out,
-                                        void* dw_bf16, void* stream) {
+                                        void* dw_bf16, void* workspace, size_t ws_bytes, void* stream) {
   if (!dy_bf16 || !xq || !x_scale || !offsets || !dw_bf16) return SBN_ERR_NULL;
   sbn_status st = check_grad(rows, offsets, experts, k, n_out);
   if (st != SBN_OK) return st;
-  if (!aligned16(dy_bf16) || !aligned16(xq) || !aligned16(dw_bf16) || (reinterpret_cast<uintptr_t>(x_scale) & 3u))
+  if (!aligned16(dy_bf16) || !aligned16(xq) || !aligned16(dw_bf16) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(x_scale) & 3u))
     return SBN_ERR_ALIGN;
+  const size_t need = sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, experts, k, n_out);
+  if (need && (!workspace || ws_bytes < need)) return SBN_ERR_WORKSPACE;
   int dev = 0, sms = 0;
   if ((st = check_device(&dev, &sms)) != SBN_OK) return st;
-  GwParams p;
+  GwParams p = {};
   p.dy = reinterpret_cast<const uint16_t*>(dy_bf16); p.xq = xq; p.xs = x_scale;
   p.dw = reinterpret_cast<uint16_t*>(dw_bf16); p.grp = GrpParams{offsets, experts, rows}; p.K = k; p.N = n_out;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const size_t list = 8 * (size_t)(experts + 1);
   if (n_out % 8 != 0) {
     const dim3 grid((unsigned)(k / kBwTile), (unsigned)((n_out + kBwTile - 1) / kBwTile), (unsigned)experts);
-    return launch_ex(bwd_dw_grp_plain_kernel, grid, dim3(kBwThreads), 8 * (size_t)(experts + 1), cs, 1, p);
+    return launch_ex(bwd_dw_grp_plain_kernel, grid, dim3(kBwThreads), list, cs, 1, p);
   }
+  const GwLayout l(rows, experts, k, n_out);
+  uint8_t* w8 = reinterpret_cast<uint8_t*>(workspace);
+  p.a16 = reinterpret_cast<uint16_t*>(w8);
+  p.x16 = reinterpret_cast<uint16_t*>(w8 + l.x16);
+  p.scale = reinterpret_cast<float*>(w8 + l.scale);
+  // the preparation: clusters along an expert's rows until two CTAs per SM
+  // scale dY, and as many CTAs again for Xq
+  const long long blocks = (long long)((n_out + kGpCols - 1) / kGpCols) * experts;
+  p.cluster = 1;
+  while (p.cluster < 8 && blocks * p.cluster < 2ll * sms && (long long)rows > 2ll * p.cluster * kGpLanes * experts)
+    p.cluster *= 2;
+  if (blocks * p.cluster > (1ll << 30)) return SBN_ERR_SHAPE;
+  p.a_ctas = (int)(blocks * p.cluster);
+  const int x_ctas = std::min(4 * sms, (int)((l.rows + 7) / 8));
+  const unsigned grid = (unsigned)((p.a_ctas + x_ctas + p.cluster - 1) / p.cluster * p.cluster);
+  if ((st = launch_ex(bwd_dw_prep_kernel, dim3(grid), dim3(kGpThreads), list, cs, (unsigned)p.cluster, p)) != SBN_OK)
+    return st;
+  CUtensorMap ta, tx;
+  if (!encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.a16, n_out, l.rows, 2 * (uint64_t)n_out, 64, kGwBK,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.x16, k, l.rows, 2 * (uint64_t)k, 64, kGwBK,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return SBN_ERR_CUDA;
   static bool attr_set[kMaxDevices] = {};
   if (!set_smem_attr_once(bwd_dw_grp_kernel, gw_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
-  const long long tiles = (long long)experts * ((n_out + kBwBM - 1) / kBwBM) * ((k + kBwBN - 1) / kBwBN);
-  const int grid = (int)std::min(tiles, (long long)sms);
-  return launch_ex(bwd_dw_grp_kernel, dim3((unsigned)grid), dim3(kTcThreads), gw_smem_bytes(experts), cs, 1, p);
+  const long long tiles = (long long)experts * ((n_out + kGwBM - 1) / kGwBM) * ((k + kGwBN - 1) / kGwBN);
+  const int main_grid = (int)std::min(tiles, (long long)sms);
+  return launch_ex(bwd_dw_grp_kernel, dim3((unsigned)main_grid), dim3(kGwThreads), gw_smem_bytes(experts), cs, 1, ta, tx,
+                   p);
 }
 
 }  // extern "C"

@@ -84,7 +84,8 @@ PROTOTYPES = {
     "sbn_bitlinear_grouped_grad_x": (ctypes.c_int, [_c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                     _c_p, _c_p, _c_p, _c_p, _c_p]),
     "sbn_bitlinear_grouped_grad_w": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_p,
-                                                    _c_p]),
+                                                    _c_p, _c_sz, _c_p]),
+    "sbn_bitlinear_grouped_grad_w_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
     "sbn_adamw": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, ctypes.c_double, _c_p,
                                  ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _c_p,
                                  ctypes.c_uint32, _c_p]),
@@ -771,8 +772,10 @@ def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedE
 
 
 def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor,
-                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """sbn_bitlinear_grouped_grad_w: dW of every expert (bf16 [E, N_out, K])."""
+                             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """sbn_bitlinear_grouped_grad_w: dW of every expert (bf16 [E, N_out, K]),
+    zero for an expert without rows."""
     _need(dy, torch.bfloat16, "dy")
     _need(xq, torch.int8, "xq")
     rows, n_out = dy.shape
@@ -785,8 +788,10 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
     _one_device(dy, xq, s, offsets, out)
     if out is None:
         out = _new((experts, n_out, k), torch.bfloat16, dy.device, stream)
+    need = int(lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, experts, k, n_out))
+    ws = _scratch(need, workspace, dy.device, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_w", stream, _ptr(dy), _ptr(xq), _ptr(s), rows, _ptr(offsets),
-            experts, k, n_out, _ptr(out))
+            experts, k, n_out, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
 
