@@ -148,9 +148,10 @@ SBN_DEVFN uint32_t gv_prmt(uint32_t a, uint32_t b, uint32_t sel) {
 // odd-indexed ones (od: code 2k+1 in byte k). Masking v with 0x3333 leaves
 // code 2k alone in nibble k, which then selects its byte of the table
 // {0, +1, 0, -1}; the odd codes are the same two bits higher.
+template <uint32_t TABLE = kCodeByteTable>
 SBN_DEVFN void gv_codes_eo(uint32_t v, uint32_t& ev, uint32_t& od) {
-  ev = gv_prmt(kCodeByteTable, 0u, v & 0x3333u);
-  od = gv_prmt(kCodeByteTable, 0u, (v >> 2) & 0x3333u);
+  ev = gv_prmt(TABLE, 0u, v & 0x3333u);
+  od = gv_prmt(TABLE, 0u, (v >> 2) & 0x3333u);
 }
 
 // Selector pair of a keep mask over (ev, od): output byte i takes kept value
@@ -186,13 +187,14 @@ SBN_DEVFN uint32_t gv_field(const uint32_t (&w)[NW]) {
 // 0-3 (w0) and 4-7 (w1). cw: the span's code words; mw: its 8 keep bytes;
 // s_sel2: the selector pairs of the 256 keep masks, COPIES of each in a row
 // (a reader with its own copy meets fewer bank conflicts).
-template <int MM, int CB, bool DENSE, int I, int COPIES = 1>
+// TABLE: the byte each code becomes (0 for a pruned position).
+template <int MM, int CB, bool DENSE, int I, int COPIES = 1, uint32_t TABLE = kCodeByteTable>
 SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* s_sel2, uint32_t& w0,
                          uint32_t& w1) {
   if constexpr (DENSE) {
     // n == m: 8 codes per group, no keep bits; interleave even and odd
     uint32_t ev, od;
-    gv_codes_eo(gv_bits<16 * I, 16, CB>(cw), ev, od);
+    gv_codes_eo<TABLE>(gv_bits<16 * I, 16, CB>(cw), ev, od);
     w0 = gv_prmt(ev, od, 0x5140u);
     w1 = gv_prmt(ev, od, 0x7362u);
     return;
@@ -202,8 +204,8 @@ SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], cons
     constexpr int kOff = 4 * CB * I;
     constexpr uint32_t kMask = CB == 1 ? 0x3u : CB == 2 ? 0x33u : 0x333u;
     const uint32_t m8 = gv_prmt(mw[I / 4], 0u, 0x4440u | (I % 4));
-    const uint32_t ev = gv_prmt(kCodeByteTable, 0u, gv_field<kOff, kMask, CB>(cw));
-    const uint32_t od = gv_prmt(kCodeByteTable, 0u, gv_field<kOff + 2, kMask, CB>(cw));
+    const uint32_t ev = gv_prmt(TABLE, 0u, gv_field<kOff, kMask, CB>(cw));
+    const uint32_t od = gv_prmt(TABLE, 0u, gv_field<kOff + 2, kMask, CB>(cw));
     const uint2 sel = s_sel2[m8 * COPIES];
     w0 = gv_prmt(ev, od, sel.x);
     w1 = gv_prmt(ev, od, sel.y);
@@ -222,7 +224,7 @@ SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], cons
     }
     const uint32_t m8 = gv_prmt(mw[I / 4], 0u, 0x4440u | (I % 4));
     uint32_t ev, od;
-    gv_codes_eo(v, ev, od);
+    gv_codes_eo<TABLE>(v, ev, od);
     const uint2 sel = s_sel2[m8 * COPIES];
     w0 = gv_prmt(ev, od, sel.x);
     w1 = gv_prmt(ev, od, sel.y);

@@ -131,13 +131,24 @@ SBN_DEVFN void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
-// The k-th tile of this CTA: from the list, worked out on the spot behind it.
-SBN_DEVFN TgTile tg_get(const int4* list, const int* off, const int* first, const GrpParams& g, int k, int row_tiles) {
-  if (k >= kTgList)
-    return tg_tile(off, first, g, (int)blockIdx.x + k * (int)gridDim.x, row_tiles, kTgBM, kTgBN, 16);
+// The k-th tile of this CTA: from the list (`len` entries), worked out on the
+// spot behind it. BM, BN, STEP: tg_tile's.
+template <int BM, int BN, int STEP>
+SBN_DEVFN TgTile tg_get(const int4* list, int len, const int* off, const int* first, const GrpParams& g, int k,
+                        int row_tiles) {
+  if (k >= len) return tg_tile(off, first, g, (int)blockIdx.x + k * (int)gridDim.x, row_tiles, BM, BN, STEP);
   const int4 v = list[k];
   const int have = v.w - v.z;
-  return TgTile{v.x, v.y, v.z, v.w, have > 0 ? (have + 15) / 16 * 16 : 0};
+  return TgTile{v.x, v.y, v.z, v.w, have > 0 ? (have + STEP - 1) / STEP * STEP : 0};
+}
+// The list, by all threads of the CTA: its first `len` tiles of `count`.
+template <int BM, int BN, int STEP>
+SBN_DEVFN void tg_list(int4* list, int len, const int* off, const int* first, const GrpParams& g, int count,
+                       int row_tiles) {
+  for (int k = (int)threadIdx.x; k < min(count, len); k += (int)blockDim.x) {
+    const TgTile t = tg_tile(off, first, g, (int)blockIdx.x + k * (int)gridDim.x, row_tiles, BM, BN, STEP);
+    list[k] = make_int4(t.e, t.row0, t.tok0, t.tok_end);
+  }
 }
 
 // 64 positions (one span of bl_gemv.cuh) -> 16 words of int8.
@@ -217,10 +228,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   const uint32_t tmem = *s_tmem;
   const int n_tiles = s_first[p.grp.experts];
   const int count = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-  for (int k = tid; k < min(count, kTgList); k += kTgThreads) {
-    const TgTile t = tg_tile(s_off, s_first, p.grp, (int)blockIdx.x + k * (int)gridDim.x, row_tiles, kTgBM, kTgBN, 16);
-    s_list[k] = make_int4(t.e, t.row0, t.tok0, t.tok_end);
-  }
+  tg_list<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, count, row_tiles);
   __syncthreads();
   int used = 0;   // tiles this role has worked on
 
@@ -231,7 +239,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     uint32_t ph = 1;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
-      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       const int nmma = __shfl_sync(0xffffffffu, t.nmma, 0), tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
       for (int ks = 0; ks < nst; ++ks) {
@@ -261,7 +269,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     uint32_t ph = 1;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
-      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       // rows past the expert's are expanded, never stored
       const int row = __shfl_sync(0xffffffffu, t.e * p.N + t.row0, 0);
@@ -288,10 +296,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    TgTile t = count ? tg_get(s_list, s_off, s_first, p.grp, 0, row_tiles) : TgTile{};
+    TgTile t = count ? tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, 0, row_tiles) : TgTile{};
     for (int k = 0; k < count && ok; ++k) {
       const int nmma = t.nmma;
-      if (k + 1 < count) t = tg_get(s_list, s_off, s_first, p.grp, k + 1, row_tiles);
+      if (k + 1 < count) t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k + 1, row_tiles);
       if (!nmma) continue;
       const uint32_t idesc = __shfl_sync(0xffffffffu, kTgIdesc0 | ((uint32_t)(nmma >> 3) << 17), 0);
       const int b = used & 1;
@@ -340,7 +348,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     uint32_t ph = 0;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
-      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       // this group's stages of the tile
       const int end = it + nst;
@@ -359,10 +367,6 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
           }
           uint4 mv = make_uint4(0u, 0u, 0u, 0u);
           if (!DENSE) mv = mp[j];
-          if (j == 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_empty[s]);
-          }
           const uint32_t m0[2] = {mv.x, mv.y}, m1[2] = {mv.z, mv.w};
           uint32_t w[32];
           tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
@@ -376,7 +380,11 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         if (!ok) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        if (lane == 0) {
+          // the packed rows only now, when what was loaded of them has been used
+          mbar_arrive(&p_empty[s]);
+          mbar_arrive(&full[s]);
+        }
       }
     }
   } else if (warp >= kTgEpiWarp) {
@@ -388,7 +396,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
                reinterpret_cast<float*>(ybuf + kTgEpiWarps * 4096) + 32 * (warp - kTgEpiWarp), 0};
     const EpiOut out{&tmap_y, &tmap_z, p.y, p.N, p.grp.rows, p.aligned != 0};
     for (int k = 0; k < count; ++k) {
-      const TgTile t = tg_get(s_list, s_off, s_first, p.grp, k, row_tiles);
+      const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       const int b = used & 1;
       const int row_w = t.row0 + 32 * q;

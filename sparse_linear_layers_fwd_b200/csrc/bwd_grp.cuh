@@ -9,15 +9,22 @@
 // accumulation in tensor memory; an expert without rows has dW_e = 0, rows
 // outside the experts' ranges keep their dX.
 //
-// dX: persistent CTAs walk tiles of 128 rows of one expert x 256 positions.
-//   warp 0      TMA of dY (128 rows x 64 features per stage, K-major);
-//   warp 1      TMEM and the MMA thread;  warp 2  the work list;
-//   warps 4-11  producers: a thread expands 64 positions of one output
-//               feature of C_e (bl_gemv.cuh's expansion) to bf16, one
-//               128-byte row of the MN-major B tile;
-//   warps 12-15 epilogue.
+// dX: persistent CTAs walk tiles of 128 rows of one expert x 256 positions,
+// 64 features of the contraction per stage.
+//   warp 0      TMA of dY (128 rows x 64 features, K-major);
+//   warp 1      TMEM and the MMA warp;
+//   warp 2      the work list, then TMA of the packed rows (64 features x 256
+//               positions of codes and keep bits);
+//   warps 4-19  producers: two groups of eight warps take the stages in turn; a
+//               thread expands 64 positions of one output feature of C_e
+//               (bl_gemv.cuh's expansion) to bf16, one 128-byte row of the
+//               MN-major B tile. The byte table gives the high byte of bf16
+//               0, 1 or -1, whose low byte is its lowest bit moved up;
+//   warps 20-23 epilogue.
 // Rows of the next expert in a tile are multiplied too (rows are
-// independent) and not stored.
+// independent) and not stored. Bound by shared memory: a stage's MMAs read 48
+// KB, TMA writes 16 and the producers 32, 768 cycles at 128 bytes each beside
+// 512 cycles of MMA.
 //
 // dW in two kernels. bwd_dw_prep_kernel lays the operands out once in the
 // caller's workspace, as fp16, every expert's rows padded with zeros to a
@@ -47,10 +54,25 @@
 namespace sbn {
 
 constexpr int kGxSelCopies = kTgSelCopies;
+constexpr int kGxThreads = 768;
+constexpr int kGxEpiWarp = 20;                       // first epilogue warp
+constexpr int kGxPackedBytes = kBxBK * (64 + 32);    // packed rows of a stage
+constexpr int kGxList = 128;
+constexpr uint32_t kBf16HighTable = 0xBF003F00u;     // codes 00, 01, 10, 11 -> high byte of bf16
 
 __host__ __device__ inline size_t gx_smem_bytes(int experts) {
-  return 1024 + (size_t)kBxStages * kBxStageBytes + 256 * 8 * kGxSelCopies + (2 * kBxStages + 4) * 8 + 16 +
-         2 * 4 * (size_t)(experts + 1);
+  return 1024 + (size_t)kBxStages * kBxStageBytes + 2 * kGxPackedBytes + 256 * 8 * kGxSelCopies +
+         (2 * kBxStages + 8) * 8 + 16 + 16 * kGxList + 2 * 4 * (size_t)(experts + 1);
+}
+
+// Eight positions (group I of the span) -> eight bf16 (0, 1 or -1).
+template <int MM, int CB, bool DENSE, int I>
+SBN_DEVFN uint4 gx_expand8(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* sel) {
+  uint32_t h0, h1;
+  gv_expand<MM, CB, DENSE, I, kGxSelCopies, kBf16HighTable>(cw, mw, sel, h0, h1);
+  const uint32_t l0 = (h0 << 7) & 0x80808080u, l1 = (h1 << 7) & 0x80808080u;
+  return make_uint4(gv_prmt(l0, h0, 0x5140u), gv_prmt(l0, h0, 0x7362u), gv_prmt(l1, h1, 0x5140u),
+                    gv_prmt(l1, h1, 0x7362u));
 }
 
 struct GxParams {
@@ -64,17 +86,22 @@ struct GxParams {
 };
 
 template <int MM, int CB, bool DENSE>
-__global__ void __launch_bounds__(kTcThreads, 1)
-bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const GxParams p) {
+__global__ void __launch_bounds__(kGxThreads, 1)
+bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant__ CUtensorMap tmap_c,
+                  const __grid_constant__ CUtensorMap tmap_m, const GxParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint2* s_sel = reinterpret_cast<uint2*>(smem + (size_t)kBxStages * kBxStageBytes);
+  uint8_t* packed = smem + (size_t)kBxStages * kBxStageBytes;
+  uint2* s_sel = reinterpret_cast<uint2*>(packed + 2 * kGxPackedBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kGxSelCopies);
   uint64_t* empty = full + kBxStages;
-  uint64_t* acc_full = empty + kBxStages;   // [2]
+  uint64_t* p_full = empty + kBxStages;     // [2], one per producer group
+  uint64_t* p_empty = p_full + 2;           // [2]
+  uint64_t* acc_full = p_empty + 2;         // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
-  int* s_off = reinterpret_cast<int*>(s_tmem + 4);
+  int4* s_list = reinterpret_cast<int4*>(s_tmem + 4);
+  int* s_off = reinterpret_cast<int*>(s_list + kGxList);
   int* s_first = s_off + p.grp.experts + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -83,12 +110,14 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const GxParams p)
 
   if (tid == 0) {
     for (int s = 0; s < kBxStages; ++s) {
-      mbar_init(&full[s], kTcProducers / 32 + 1);
+      mbar_init(&full[s], 8 + 1);   // a group's warps and dY's TMA
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&p_full[b], 1);
+      mbar_init(&p_empty[b], 8);
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kTcEpilogue / 32);
+      mbar_init(&acc_empty[b], 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -107,126 +136,154 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const GxParams p)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int n_tiles = s_first[p.grp.experts], grid = (int)gridDim.x;
+  const int n_tiles = s_first[p.grp.experts];
+  const int count = n_tiles > (int)blockIdx.x ? (n_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  tg_list<kBxBN, kBxBM, 1>(s_list, kGxList, s_off, s_first, p.grp, count, col_tiles);
+  __syncthreads();
+  auto tile_at = [&](int k) { return tg_get<kBxBN, kBxBM, 1>(s_list, kGxList, s_off, s_first, p.grp, k, col_tiles); };
   int used = 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-        const TgTile t = tg_tile(s_off, s_first, p.grp, tile, col_tiles, kBxBN, kBxBM, 1);
-        if (!t.nmma) continue;
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          const int s = it % kBxStages;
-          if (!mbar_wait(&empty[s], ((it / kBxStages) & 1u) ^ 1u)) { ok = false; break; }
+    const bool lead = elect_one();
+    int s = 0;
+    uint32_t ph = 1u;
+    bool ok = true;
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tile_at(k);
+      if (!t.nmma) continue;
+      const int tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        uint8_t* st = smem + (size_t)s * kBxStageBytes;
+        if (lead) {
           mbar_arrive_expect_tx(&full[s], kBxABytes);
-          tma_load_2d(smem + (size_t)s * kBxStageBytes, &tmap_dy, ks * kBxBK, t.tok0, &full[s]);
+          tma_load_2d(st, &tmap_dy, ks * kBxBK, tok0, &full[s]);
         }
+        __syncwarp();
+        if (++s == kBxStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 2) {
+    const bool lead = elect_one();
+    int it = 0;
+    bool ok = true;
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tile_at(k);
+      if (!t.nmma) continue;
+      // rows past the expert's (of the next, or zeros) meet zeros of dY
+      const int row = __shfl_sync(0xffffffffu, t.e * p.N, 0), k0 = __shfl_sync(0xffffffffu, t.row0, 0);
+      for (int ks = 0; ks < nst; ++ks, ++it) {
+        const int g = it & 1;
+        if (!mbar_wait(&p_empty[g], ((it >> 1) & 1u) ^ 1u)) { ok = false; break; }
+        uint8_t* dst = packed + g * kGxPackedBytes;
+        if (lead) {
+          mbar_arrive_expect_tx(&p_full[g], (uint32_t)(kBxBK * (16 * CB + (DENSE ? 0 : 32))));
+          tma_load_2d(dst, &tmap_c, k0 / 16 * CB, row + ks * kBxBK, &p_full[g]);
+          if (!DENSE) tma_load_2d(dst + kBxBK * 64, &tmap_m, k0 / 8, row + ks * kBxBK, &p_full[g]);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-        const TgTile t = tg_tile(s_off, s_first, p.grp, tile, col_tiles, kBxBN, kBxBM, 1);
-        if (!t.nmma) continue;
-        const int b = used & 1;
-        if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+    // ---- MMA issuer: the whole warp runs the loop, one elected lane issues ----
+    const bool lead = elect_one();
+    const uint32_t base = smem_u32(smem);
+    const uint64_t ad0 = sw128_kmajor_desc(base), bd0 = sw128_mnmajor_desc(base + kBxABytes, 1024u, 4096u);
+    int s = 0;
+    uint32_t ph = 0u;
+    bool ok = true;
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tile_at(k);
+      if (!t.nmma) continue;
+      const int b = used & 1;
+      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      const uint32_t d_tmem = tmem + (uint32_t)(b * kBxBN);
+      for (int ks = 0; ks < nst; ++ks) {
+        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)(b * kBxBN);
-        for (int ks = 0; ks < nst; ++ks, ++it) {
-          const int s = it % kBxStages;
-          if (!mbar_wait(&full[s], (it / kBxStages) & 1u)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + (size_t)s * kBxStageBytes);
-          const uint64_t adesc = sw128_kmajor_desc(a_addr);
-          const uint64_t bdesc = sw128_mnmajor_desc(a_addr + kBxABytes, 1024u, 4096u);
+        const uint64_t so = (uint64_t)(s * (kBxStageBytes / 16));
+        if (lead) {
 #pragma unroll
-          for (int k = 0; k < kBxBK / 16; ++k)
-            tc_mma_f16(d_tmem, adesc + (uint64_t)(2 * k), bdesc + (uint64_t)(k * (8192 / 16)),
-                       (ks > 0 || k > 0) ? 1u : 0u);
+          for (int i = 0; i < kBxBK / 16; ++i)
+            tc_mma_f16(d_tmem, ad0 + so + (uint64_t)(2 * i), bd0 + so + (uint64_t)(i * (8192 / 16)),
+                       (ks > 0 || i > 0) ? 1u : 0u);
           tc_commit(&empty[s]);
         }
-        tc_commit(&acc_full[b]);
-        ++used;
+        __syncwarp();
+        if (++s == kBxStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      for (int j = used - 2; j < used; ++j)
-        if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
+      if (lead) tc_commit(&acc_full[b]);
+      __syncwarp();
+      ++used;
     }
+    for (int j = used - 2; j < used; ++j)
+      if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
     __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
-    // ---- producers: thread (feature ol of the stage, span q of 64 positions) ----
-    const int pi = tid - 128, ol = pi & 63, q = pi >> 6;
+  } else if (warp >= 4 && warp < kGxEpiWarp) {
+    // ---- producers: group g takes the stages with index = g (mod 2), counted
+    // over all tiles; thread = (feature ol of the stage, span q of 64 positions) ----
+    const int g = (warp - 4) >> 3, pi = tid - 128 - 256 * g, ol = pi & 63, q = pi >> 6;
     const uint2* sel = s_sel + (lane & (kGxSelCopies - 1));
     const int r = ol & 7;
+    const uint32_t* cp = reinterpret_cast<const uint32_t*>(packed + g * kGxPackedBytes + ol * 16 * CB + q * 4 * CB);
+    const uint2* mp = reinterpret_cast<const uint2*>(packed + g * kGxPackedBytes + kBxBK * 64 + ol * 32 + q * 8);
+    uint8_t* const row0 = smem + kBxABytes + (size_t)(ol >> 3) * 4096 + (size_t)q * 1024 + (size_t)r * 128;
     int it = 0;
+    uint32_t ph = 0u;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < n_tiles && ok; tile += grid) {
-      const TgTile t = tg_tile(s_off, s_first, p.grp, tile, col_tiles, kBxBN, kBxBM, 1);
+    for (int k = 0; k < count && ok; ++k) {
+      const TgTile t = tile_at(k);
       if (!t.nmma) continue;
-      const int k0 = t.row0 + 64 * q;   // first position of the span
-      const bool in_k = k0 < p.K;
-      const uint8_t* crow = p.codes + (size_t)t.e * p.N * p.cstride + (size_t)(k0 >> 4) * CB;
-      const uint8_t* mrow = DENSE ? nullptr : p.meta + (size_t)t.e * p.N * p.mstride + (k0 >> 3);
-      uint32_t cn[CB], mn[2];
-      auto load = [&](int ks) {
-        const int o = ks * kBxBK + ol;
+      const int end = it + nst;
+      int mine = it + ((it ^ g) & 1);
+      it = end;
+      for (; mine < end; mine += 2, ph ^= 1u) {
+        if (!mbar_wait(&p_full[g], ph)) { ok = false; break; }
+        uint32_t cw[CB], mw[2] = {0u, 0u};
 #pragma unroll
-        for (int j = 0; j < CB; ++j) cn[j] = 0u;
-        mn[0] = mn[1] = 0u;
-        if (o < p.N && in_k) {
-          const uint32_t* cp = reinterpret_cast<const uint32_t*>(crow + (size_t)o * p.cstride);
-#pragma unroll
-          for (int j = 0; j < CB; ++j) cn[j] = __ldg(cp + j);
-          if (!DENSE) {
-            const uint2 m = __ldg(reinterpret_cast<const uint2*>(mrow + (size_t)o * p.mstride));
-            mn[0] = m.x;
-            mn[1] = m.y;
-          }
+        for (int j = 0; j < CB; ++j) cw[j] = cp[j];
+        if (!DENSE) {
+          const uint2 m = *mp;
+          mw[0] = m.x;
+          mw[1] = m.y;
         }
-      };
-      load(0);
-      for (int ks = 0; ks < nst; ++ks, ++it) {
-        const int s = it % kBxStages;
-        uint32_t cw[CB], mw[2] = {mn[0], mn[1]};
-#pragma unroll
-        for (int j = 0; j < CB; ++j) cw[j] = cn[j];
-        if (ks + 1 < nst) load(ks + 1);
-        uint32_t w[16];
-        tg_expand64<MM, CB, DENSE>(cw, mw, sel, w);
-        int got = 1;
-        if (lane == 0) got = mbar_wait(&empty[s], ((it / kBxStages) & 1u) ^ 1u) ? 1 : 0;
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) { ok = false; break; }
-        uint8_t* row = smem + (size_t)s * kBxStageBytes + kBxABytes + (size_t)(ol >> 3) * 4096 + (size_t)q * 1024 +
-                       (size_t)r * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t h[4];
-          s8x4_to_bf16x4(w[2 * c], h[0], h[1]);
-          s8x4_to_bf16x4(w[2 * c + 1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(row + ((c ^ r) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        const int s = mine % kBxStages;
+        if (!mbar_wait(&empty[s], ((mine / kBxStages) & 1u) ^ 1u)) { ok = false; break; }
+        uint8_t* row = row0 + (size_t)s * kBxStageBytes;
+        *reinterpret_cast<uint4*>(row + ((0 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 0>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((1 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 1>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((2 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 2>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((3 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 3>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((4 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 4>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((5 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 5>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((6 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 6>(cw, mw, sel);
+        *reinterpret_cast<uint4*>(row + ((7 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 7>(cw, mw, sel);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        if (lane == 0) {
+          // only now: handed back right behind the loads above, the packed rows
+          // were overwritten before every lane's loads had been done
+          mbar_arrive(&p_empty[g]);
+          mbar_arrive(&full[s]);
+        }
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= kGxEpiWarp) {
     const int q = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-    for (int tile = blockIdx.x; tile < n_tiles; tile += grid) {
-      const TgTile t = tg_tile(s_off, s_first, p.grp, tile, col_tiles, kBxBN, kBxBM, 1);
+    for (int k = 0; k < count; ++k) {
+      const TgTile t = tile_at(k);
       if (!t.nmma) continue;
       const int b = used & 1;
       const int row = t.tok0 + 32 * q + lane;
-      const float g = __ldg(p.gamma + t.e);
-      int got = 1;
-      if (lane == 0) got = mbar_wait(&acc_full[b], (used >> 1) & 1u) ? 1 : 0;
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) break;
+      const float gm = __ldg(p.gamma + t.e);
+      if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1
@@ -238,8 +295,8 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const GxParams p)
           uint32_t o16[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            o16[e] = (uint32_t)f32_to_bf16_bits(__fmul_rn(g, __uint_as_float(r[2 * e]))) |
-                     ((uint32_t)f32_to_bf16_bits(__fmul_rn(g, __uint_as_float(r[2 * e + 1]))) << 16);
+            o16[e] = (uint32_t)f32_to_bf16_bits(__fmul_rn(gm, __uint_as_float(r[2 * e]))) |
+                     ((uint32_t)f32_to_bf16_bits(__fmul_rn(gm, __uint_as_float(r[2 * e + 1]))) << 16);
           uint4* dst = reinterpret_cast<uint4*>(p.dx + (size_t)row * p.K + kc);
 #pragma unroll
           for (int e = 0; e < 4; ++e) dst[e] = make_uint4(o16[4 * e], o16[4 * e + 1], o16[4 * e + 2], o16[4 * e + 3]);
@@ -395,10 +452,17 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
     const bool ok = r < s_off[e + 1];
     const uint4* src = reinterpret_cast<const uint4*>(p.xq + (size_t)r * p.K);
     uint4* d = reinterpret_cast<uint4*>(p.x16 + (size_t)pr * p.K);
-    for (int c = lane; c < p.K / 16; c += 32) {
-      const uint4 v = ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    for (int c0 = lane; c0 < p.K / 16; c0 += 128) {
+      uint4 vv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        vv[u] = ok && c0 + 32 * u < p.K / 16 ? __ldg(src + c0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+      const int c = c0 + 32 * u;
+      if (c >= p.K / 16) break;
       uint32_t h[8];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t w[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         // bytes b + 128 as the low mantissa bits of 1024: exact, then - 1152
@@ -409,6 +473,7 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
       }
       d[2 * c] = make_uint4(h[0], h[1], h[2], h[3]);
       d[2 * c + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+      }
     }
   }
   griddep_launch_dependents();

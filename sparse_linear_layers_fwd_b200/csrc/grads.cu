@@ -27,13 +27,20 @@ struct LaunchDx {
     static bool attr_set[kMaxDevices] = {};
     auto kern = bwd_dx_grp_kernel<MM, CB, DENSE>;
     if (!set_smem_attr_once(kern, gx_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
-    CUtensorMap tm;
-    if (!encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, p.N, r, 2 * (uint64_t)p.N, kBxBK, kBxBM,
-                   CU_TENSOR_MAP_SWIZZLE_128B))
+    CUtensorMap td, tc, tm;
+    const uint64_t wrows = (uint64_t)e * (uint64_t)p.N;
+    if (!encode_2d(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, p.N, r, 2 * (uint64_t)p.N, kBxBK, kBxBM,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, p.cstride, wrows, p.cstride, 16 * CB, kBxBK,
+                   CU_TENSOR_MAP_SWIZZLE_NONE))
+      return SBN_ERR_CUDA;
+    tm = tc;   // unused for n == m
+    if (!DENSE && !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.meta, p.mstride, wrows, p.mstride, 32, kBxBK,
+                             CU_TENSOR_MAP_SWIZZLE_NONE))
       return SBN_ERR_CUDA;
     const long long most = (long long)(r / kBxBM + std::min(e, r)) * ((p.K + kBxBN - 1) / kBxBN);
     const int grid = (int)std::max(1LL, std::min(most, (long long)sms));
-    return launch_ex(kern, dim3((unsigned)grid), dim3(kTcThreads), gx_smem_bytes(e), st, 1, tm, p);
+    return launch_ex(kern, dim3((unsigned)grid), dim3(kGxThreads), gx_smem_bytes(e), st, 1, td, tc, tm, p);
   }
 };
 
@@ -118,11 +125,11 @@ sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, c
   p.a16 = reinterpret_cast<uint16_t*>(w8);
   p.x16 = reinterpret_cast<uint16_t*>(w8 + l.x16);
   p.scale = reinterpret_cast<float*>(w8 + l.scale);
-  // the preparation: clusters along an expert's rows until two CTAs per SM
+  // the preparation: clusters along an expert's rows until four CTAs per SM
   // scale dY, and as many CTAs again for Xq
   const long long blocks = (long long)((n_out + kGpCols - 1) / kGpCols) * experts;
   p.cluster = 1;
-  while (p.cluster < 8 && blocks * p.cluster < 2ll * sms && (long long)rows > 2ll * p.cluster * kGpLanes * experts)
+  while (p.cluster < 8 && blocks * p.cluster < 4ll * sms && (long long)rows > 2ll * p.cluster * kGpLanes * experts)
     p.cluster *= 2;
   if (blocks * p.cluster > (1ll << 30)) return SBN_ERR_SHAPE;
   p.a_ctas = (int)(blocks * p.cluster);
