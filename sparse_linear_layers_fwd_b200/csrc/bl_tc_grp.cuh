@@ -60,18 +60,19 @@ constexpr int kTgStageBytes = 2 * kTgSub;
 constexpr uint32_t kTgACol = 2 * kTgBN;        // A slots after the accumulators
 static_assert(kTgACol + 64 * kTgStages <= kTcTmemCols, "accumulators and A slots fit in TMEM");
 static_assert(kTgSub % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
-constexpr int kTgPackedBytes = kTgBM * (64 + 32);   // packed rows of a stage
+constexpr int kTgPackedBytes = kTgBM * (48 + 32);   // packed rows of a stage, at most (6:8; n == m: 64 and no keep bits)
+constexpr int kTgPacked = 5;                   // their ring: a slot is free only when its stage is expanded
 constexpr int kTgThreads = 768;
 constexpr int kTgEpiWarp = 16;                 // first epilogue warp
 constexpr int kTgSelCopies = 4;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgYBuf = kTgEpiWarps * (4096 + 128);
-constexpr int kTgBars = 4 * kTgStages + 4;
-constexpr int kTgList = 256;                   // tiles of a CTA whose place is worked out ahead
+constexpr int kTgBars = 2 * (kTgStages + kTgPacked) + 4;
+constexpr int kTgList = 64;                    // tiles of a CTA whose place is worked out ahead
 constexpr uint32_t kTgIdesc0 = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTgBM >> 4) << 24);
 
 __host__ __device__ inline size_t tg_smem_bytes(int experts) {
-  return 1024 + (size_t)kTgStages * (kTgStageBytes + kTgPackedBytes) + kTgYBuf + 256 * 8 * kTgSelCopies +
+  return 1024 + (size_t)kTgStages * kTgStageBytes + (size_t)kTgPacked * kTgPackedBytes + kTgYBuf + 256 * 8 * kTgSelCopies +
          kTgBars * 8 + 16 + 16 * kTgList + 2 * 4 * (size_t)(experts + 1);
 }
 
@@ -173,13 +174,13 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* packed = smem + (size_t)kTgStages * kTgStageBytes;
-  uint8_t* ybuf = packed + kTgStages * kTgPackedBytes;
+  uint8_t* ybuf = packed + kTgPacked * kTgPackedBytes;
   uint2* s_sel = reinterpret_cast<uint2*>(ybuf + kTgYBuf);   // [256][kTgSelCopies]
   uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
   uint64_t* empty = full + kTgStages;
   uint64_t* p_full = empty + kTgStages;
-  uint64_t* p_empty = p_full + kTgStages;
-  uint64_t* acc_full = p_empty + kTgStages;   // [2]
+  uint64_t* p_empty = p_full + kTgPacked;
+  uint64_t* acc_full = p_empty + kTgPacked;   // [2]
   uint64_t* acc_empty = acc_full + 2;         // [2]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
   int4* s_list = reinterpret_cast<int4*>(s_tmem + 4);
@@ -195,6 +196,8 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     for (int s = 0; s < kTgStages; ++s) {
       mbar_init(&full[s], 4 + 1);   // the stage's producer warps and the activations' TMA
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kTgPacked; ++s) {
       mbar_init(&p_full[s], 1);
       mbar_init(&p_empty[s], 4);
     }
@@ -279,10 +282,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         if (lead) {
           mbar_arrive_expect_tx(&p_full[s], (uint32_t)(kTgBM * (16 * CB + (DENSE ? 0 : 32))));
           tma_load_2d(dst, &tmap_c, ks * 16 * CB, row, &p_full[s]);
-          if (!DENSE) tma_load_2d(dst + kTgBM * 64, &tmap_m, ks * 32, row, &p_full[s]);
+          if (!DENSE) tma_load_2d(dst + kTgBM * 16 * CB, &tmap_m, ks * 32, row, &p_full[s]);
         }
         __syncwarp();
-        if (++s == kTgStages) {
+        if (++s == kTgPacked) {
           s = 0;
           ph ^= 1u;
         }
@@ -342,8 +345,6 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     const int i = 32 * q + lane;
     const uint2* sel = s_sel + (lane & (kTgSelCopies - 1));
     const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)s + ((uint32_t)(32 * q) << 16);
-    const uint2* cp = reinterpret_cast<const uint2*>(packed + s * kTgPackedBytes + i * 16 * CB);
-    const uint4* mp = reinterpret_cast<const uint4*>(packed + s * kTgPackedBytes + kTgBM * 64 + i * 32);
     int it = 0;   // stages over all tiles
     uint32_t ph = 0;
     bool ok = true;
@@ -355,7 +356,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       int mine = it + (s - it % kTgStages + kTgStages) % kTgStages;
       it = end;
       for (; mine < end; mine += kTgStages, ph ^= 1u) {
-        if (!mbar_wait(&p_full[s], ph)) { ok = false; break; }
+        const int ps = mine % kTgPacked;
+        if (!mbar_wait(&p_full[ps], (mine / kTgPacked) & 1u)) { ok = false; break; }
+        const uint2* cp = reinterpret_cast<const uint2*>(packed + ps * kTgPackedBytes + i * 16 * CB);
+        const uint4* mp = reinterpret_cast<const uint4*>(packed + ps * kTgPackedBytes + kTgBM * 16 * CB + i * 32);
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
           uint32_t cw[2][CB];
@@ -382,7 +386,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         __syncwarp();
         if (lane == 0) {
           // the packed rows only now, when what was loaded of them has been used
-          mbar_arrive(&p_empty[s]);
+          mbar_arrive(&p_empty[ps]);
           mbar_arrive(&full[s]);
         }
       }

@@ -56,13 +56,14 @@ namespace sbn {
 constexpr int kGxSelCopies = kTgSelCopies;
 constexpr int kGxThreads = 768;
 constexpr int kGxEpiWarp = 20;                       // first epilogue warp
-constexpr int kGxPackedBytes = kBxBK * (64 + 32);    // packed rows of a stage
-constexpr int kGxList = 128;
+constexpr int kGxPackedBytes = kBxBK * (48 + 32);    // packed rows of a stage, at most (6:8)
+constexpr int kGxPacked = 3;                         // their ring
+constexpr int kGxList = 32;
 constexpr uint32_t kBf16HighTable = 0xBF003F00u;     // codes 00, 01, 10, 11 -> high byte of bf16
 
 __host__ __device__ inline size_t gx_smem_bytes(int experts) {
-  return 1024 + (size_t)kBxStages * kBxStageBytes + 2 * kGxPackedBytes + 256 * 8 * kGxSelCopies +
-         (2 * kBxStages + 8) * 8 + 16 + 16 * kGxList + 2 * 4 * (size_t)(experts + 1);
+  return 1024 + (size_t)kBxStages * kBxStageBytes + kGxPacked * kGxPackedBytes + 256 * 8 * kGxSelCopies +
+         (2 * (kBxStages + kGxPacked) + 4) * 8 + 16 + 16 * kGxList + 2 * 4 * (size_t)(experts + 1);
 }
 
 // Eight positions (group I of the span) -> eight bf16 (0, 1 or -1).
@@ -92,12 +93,12 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* packed = smem + (size_t)kBxStages * kBxStageBytes;
-  uint2* s_sel = reinterpret_cast<uint2*>(packed + 2 * kGxPackedBytes);
+  uint2* s_sel = reinterpret_cast<uint2*>(packed + kGxPacked * kGxPackedBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kGxSelCopies);
   uint64_t* empty = full + kBxStages;
-  uint64_t* p_full = empty + kBxStages;     // [2], one per producer group
-  uint64_t* p_empty = p_full + 2;           // [2]
-  uint64_t* acc_full = p_empty + 2;         // [2]
+  uint64_t* p_full = empty + kBxStages;
+  uint64_t* p_empty = p_full + kGxPacked;
+  uint64_t* acc_full = p_empty + kGxPacked;   // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
   int4* s_list = reinterpret_cast<int4*>(s_tmem + 4);
@@ -113,9 +114,11 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       mbar_init(&full[s], 8 + 1);   // a group's warps and dY's TMA
       mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < kGxPacked; ++s) {
+      mbar_init(&p_full[s], 1);
+      mbar_init(&p_empty[s], 8);
+    }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&p_full[b], 1);
-      mbar_init(&p_empty[b], 8);
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 4);
     }
@@ -176,13 +179,13 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       // rows past the expert's (of the next, or zeros) meet zeros of dY
       const int row = __shfl_sync(0xffffffffu, t.e * p.N, 0), k0 = __shfl_sync(0xffffffffu, t.row0, 0);
       for (int ks = 0; ks < nst; ++ks, ++it) {
-        const int g = it & 1;
-        if (!mbar_wait(&p_empty[g], ((it >> 1) & 1u) ^ 1u)) { ok = false; break; }
-        uint8_t* dst = packed + g * kGxPackedBytes;
+        const int s = it % kGxPacked;
+        if (!mbar_wait(&p_empty[s], ((it / kGxPacked) & 1u) ^ 1u)) { ok = false; break; }
+        uint8_t* dst = packed + s * kGxPackedBytes;
         if (lead) {
-          mbar_arrive_expect_tx(&p_full[g], (uint32_t)(kBxBK * (16 * CB + (DENSE ? 0 : 32))));
-          tma_load_2d(dst, &tmap_c, k0 / 16 * CB, row + ks * kBxBK, &p_full[g]);
-          if (!DENSE) tma_load_2d(dst + kBxBK * 64, &tmap_m, k0 / 8, row + ks * kBxBK, &p_full[g]);
+          mbar_arrive_expect_tx(&p_full[s], (uint32_t)(kBxBK * (16 * CB + (DENSE ? 0 : 32))));
+          tma_load_2d(dst, &tmap_c, k0 / 16 * CB, row + ks * kBxBK, &p_full[s]);
+          if (!DENSE) tma_load_2d(dst + kBxBK * 16 * CB, &tmap_m, k0 / 8, row + ks * kBxBK, &p_full[s]);
         }
         __syncwarp();
       }
@@ -231,11 +234,8 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
     const int g = (warp - 4) >> 3, pi = tid - 128 - 256 * g, ol = pi & 63, q = pi >> 6;
     const uint2* sel = s_sel + (lane & (kGxSelCopies - 1));
     const int r = ol & 7;
-    const uint32_t* cp = reinterpret_cast<const uint32_t*>(packed + g * kGxPackedBytes + ol * 16 * CB + q * 4 * CB);
-    const uint2* mp = reinterpret_cast<const uint2*>(packed + g * kGxPackedBytes + kBxBK * 64 + ol * 32 + q * 8);
     uint8_t* const row0 = smem + kBxABytes + (size_t)(ol >> 3) * 4096 + (size_t)q * 1024 + (size_t)r * 128;
     int it = 0;
-    uint32_t ph = 0u;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
       const TgTile t = tile_at(k);
@@ -243,8 +243,11 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       const int end = it + nst;
       int mine = it + ((it ^ g) & 1);
       it = end;
-      for (; mine < end; mine += 2, ph ^= 1u) {
-        if (!mbar_wait(&p_full[g], ph)) { ok = false; break; }
+      for (; mine < end; mine += 2) {
+        const int ps = mine % kGxPacked;
+        if (!mbar_wait(&p_full[ps], (mine / kGxPacked) & 1u)) { ok = false; break; }
+        const uint32_t* cp = reinterpret_cast<const uint32_t*>(packed + ps * kGxPackedBytes + ol * 16 * CB + q * 4 * CB);
+        const uint2* mp = reinterpret_cast<const uint2*>(packed + ps * kGxPackedBytes + kBxBK * 16 * CB + ol * 32 + q * 8);
         uint32_t cw[CB], mw[2] = {0u, 0u};
 #pragma unroll
         for (int j = 0; j < CB; ++j) cw[j] = cp[j];
@@ -269,7 +272,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
         if (lane == 0) {
           // only now: handed back right behind the loads above, the packed rows
           // were overwritten before every lane's loads had been done
-          mbar_arrive(&p_empty[g]);
+          mbar_arrive(&p_empty[ps]);
           mbar_arrive(&full[s]);
         }
       }

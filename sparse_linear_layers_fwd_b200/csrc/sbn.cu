@@ -522,12 +522,15 @@ sbn_status launch_tc2(const CUtensorMap& tm, const CUtensorMap& tw, const CUtens
 // per-stage cost in the MMA thread) counted as 0.6 of a 256-token one. The
 // narrow tiles win where the wide ones leave pairs idle (few tiles, or a
 // short last wave).
-bool tc2_narrow_pays(int t, int n_out, int wide_pairs, int narrow_pairs) {
+// With an epilogue (epi) the epilogue sets the pace, and a narrow tile costs
+// half a wide one (2048 x 4864, K = 896: 5 rounds of narrow tiles against 3 of
+// wide ones).
+bool tc2_narrow_pays(int t, int n_out, int wide_pairs, int narrow_pairs, bool epi) {
   if (narrow_pairs <= 0) return false;
   const long long rp = (n_out + 255) / 256;
   const long long wide = rp * ((t + 255) / 256), narrow = rp * ((t + 127) / 128);
   const long long rw = (wide + wide_pairs - 1) / wide_pairs, rn = (narrow + narrow_pairs - 1) / narrow_pairs;
-  return 6 * rn < 10 * rw;
+  return epi ? rn < 2 * rw : 6 * rn < 10 * rw;
 }
 
 // 2:4 weights on the sparse tensor-core MMA: expanded once into the
@@ -571,7 +574,7 @@ sbn_status run_bitlinear_pairs(const int8_t* xq, const TcParams& p, int n, int m
   if (s2 != SBN_OK) return s2;
   if ((s2 = make_weight_tensor_map(&tw, wd, p.N, p.K)) != SBN_OK) return s2;
   const int npairs = tc2_max_pairs<false, ACC_OUT, true, EPI>();
-  if (tc2_narrow_pays(p.T, p.N, pairs, npairs)) {
+  if (tc2_narrow_pays(p.T, p.N, pairs, npairs, EPI)) {
     if ((s2 = make_act_tensor_map(&tm, xq, p.T, p.K, T2Cfg<false, true>::HALF)) != SBN_OK) return s2;
     return launch_tc2<false, ACC_OUT, true, EPI>(tm, tw, tw, p, npairs, st, ep);
   }

@@ -535,38 +535,38 @@ def _act_buffers(x, rows: int, w, lead, bias, residual, out, out_z, stream):
     _need_shape(out_z, torch.bfloat16, (rows, w.n_out), "out_z")
     _one_device(x, bias, residual, out, out_z)
     _apart(out_z, out, residual)
-    return _new((rows, w.n_out), torch.bfloat16, x.device, stream) if out is None else out
+    return _new((rows, w.n_out), torch.bfloat16, x, stream) if out is None else out
 
 
-def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
-    """An uninitialized tensor that belongs to the call's stream."""
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An uninitialized tensor on the device of `like` that belongs to the call's stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with _alloc_on(dev, stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
+    with _alloc_on(like.device, stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(need: int, workspace, dev: torch.device, stream):
+def _scratch(need: int, workspace, like: torch.Tensor, stream):
     if workspace is None:
-        return _new((need,), torch.uint8, dev, stream) if need else None
+        return _new((need,), torch.uint8, like, stream) if need else None
     _need(workspace, torch.uint8, "workspace")
-    if workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
+    if workspace.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
     return workspace
 
 
-def _run_with_scratch(dev: torch.device, name: str, stream, try_without: bool, workspace, need, args) -> None:
+def _run_with_scratch(like: torch.Tensor, name: str, stream, try_without: bool, workspace, need, args) -> None:
     """A call whose workspace is last among its arguments. A decode call mostly
     needs none: it is tried without one first (the library refuses it before
     anything is enqueued) when the caller gave none."""
     if workspace is None and try_without:
-        st = _status_on(dev, name, stream, *args, None, 0)
+        st = _status_on(like.device, name, stream, *args, None, 0)
         if st == 0:
             return
         if SBN_STATUS[st] != "SBN_ERR_WORKSPACE":
             raise SbnError(st, name)
-    ws = _scratch(need(), workspace, dev, stream)
-    _run_on(dev, name, stream, *args, _ptr(ws), ws.numel())
+    ws = _scratch(need(), workspace, like, stream)
+    _run_on(like.device, name, stream, *args, _ptr(ws), ws.numel())
 
 
 def bitlinear_act(xq: torch.Tensor, s: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tensor] = None,
@@ -587,7 +587,7 @@ def bitlinear_act(xq: torch.Tensor, s: torch.Tensor, w: PackedWeights, bias: Opt
     out = _act_buffers(xq, t, w, (), bias, residual, out, out_z, stream)
     ws = None
     if workspace is not False:
-        ws = _scratch(bitlinear_workspace_bytes(t, k, w.n_out), workspace, xq.device, stream)
+        ws = _scratch(bitlinear_workspace_bytes(t, k, w.n_out), workspace, xq, stream)
     _run_on(xq.device, "sbn_bitlinear_act", stream, _ptr(xq), _ptr(s), t, k, w.n_out, w.n, w.m, _ptr(w.codes),
             _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(ws),
             0 if ws is None else ws.numel())
@@ -612,7 +612,7 @@ def bitlinear_x_act(x: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tens
     out = _act_buffers(x, t, w, (), bias, residual, out, out_z, stream)
     args = (_ptr(x), t, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code,
             _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s))
-    _run_with_scratch(x.device, "sbn_bitlinear_x_act", stream, t <= 16, workspace,
+    _run_with_scratch(x, "sbn_bitlinear_x_act", stream, t <= 16, workspace,
                       lambda: bitlinear_x_workspace_bytes(t, k, w.n_out), args)
     return out
 
@@ -633,9 +633,9 @@ def act_grad(dy: torch.Tensor, z: torch.Tensor, act: str, offsets: Optional[torc
         experts = _experts_of(offsets)
         lead = (experts,)
     if out is None:
-        out = _new((rows, n_out), torch.bfloat16, dy.device, stream)
+        out = _new((rows, n_out), torch.bfloat16, dy, stream)
     if out_bias is None:
-        out_bias = _new(lead + (n_out,), torch.float32, dy.device, stream)
+        out_bias = _new(lead + (n_out,), torch.float32, dy, stream)
     dbias = None if out_bias is False else out_bias
     _need_shape(dbias, torch.float32, lead + (n_out,), "out_bias")
     _one_device(dy, z, offsets, out, dbias)
@@ -747,7 +747,7 @@ def bitlinear_grouped_x(x: torch.Tensor, offsets: torch.Tensor, w: PackedExperts
     out = _act_buffers(x, rows, w, (w.experts,), bias, residual, out, out_z, stream)
     args = (_ptr(x), rows, _ptr(offsets), w.experts, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta),
             _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s))
-    _run_with_scratch(x.device, "sbn_bitlinear_grouped_x", stream, rows <= 16, workspace,
+    _run_with_scratch(x, "sbn_bitlinear_grouped_x", stream, rows <= 16, workspace,
                       lambda: int(lib().sbn_bitlinear_grouped_x_workspace_bytes(rows, k)), args)
     return out
 
@@ -765,7 +765,7 @@ def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedE
     _need_packed(w, dy.device)
     _one_device(dy, offsets, out)
     if out is None:
-        out = _new((rows, w.k), torch.bfloat16, dy.device, stream)
+        out = _new((rows, w.k), torch.bfloat16, dy, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_x", stream, _ptr(dy), rows, _ptr(offsets), w.experts, w.k, n_out,
             w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(out))
     return out
@@ -787,9 +787,9 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
     _need_shape(out, torch.bfloat16, (experts, n_out, k), "out")
     _one_device(dy, xq, s, offsets, out)
     if out is None:
-        out = _new((experts, n_out, k), torch.bfloat16, dy.device, stream)
+        out = _new((experts, n_out, k), torch.bfloat16, dy, stream)
     need = int(lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, experts, k, n_out))
-    ws = _scratch(need, workspace, dy.device, stream)
+    ws = _scratch(need, workspace, dy, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_w", stream, _ptr(dy), _ptr(xq), _ptr(s), rows, _ptr(offsets),
             experts, k, n_out, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel())
     return out
@@ -811,9 +811,10 @@ class AdamW:
     per 256 elements, rounded stochastically from `seed`, the step, the position
     of the tensor in the list and the index of the element.
 
-    The state lives in m, v, m_scales, v_scales (lists, in the order of
-    params) and step (int32 [2] on the device: completed steps and a word of
-    the library); state_dict() / load_state_dict() copy it. lr is a float, or
+    The state lives in m, v, m_scales, v_scales (tuples, in the order of
+    params; assigning a sequence replaces them) and step_state (int32 [2] on the
+    device: completed steps and a word of the library); state_dict() and
+    load_state_dict() copy it. lr is a float, or
     an fp32 device tensor of one element that a captured graph reads anew at
     every replay.
     """
@@ -847,16 +848,61 @@ class AdamW:
                 if c.numel() != p.numel():
                     raise ValueError("a copy and its parameter differ in size")
             _one_device(self.params[0], *self.copies)
-        kw = dict(device=self.device)
+        self._sizes = [p.numel() for p in self.params]
+        # entries of sbn_adamw_tensor: eight 64-bit words each
+        self._table = array.array("q", bytes(64 * len(self.params)))
+        self._table[7::8] = array.array("q", self._sizes)
         st = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
-        self.m = [torch.zeros(p.numel(), dtype=st, **kw) for p in self.params]
-        self.v = [torch.zeros(p.numel(), dtype=st, **kw) for p in self.params]
-        self.m_scales = self.v_scales = None
+        like = self.params[0]
+        self.m = [like.new_zeros(n, dtype=st) for n in self._sizes]
+        self.v = [like.new_zeros(n, dtype=st) for n in self._sizes]
         if state_bits == 8:
-            blocks = [-(-p.numel() // ADAMW_BLOCK) for p in self.params]
-            self.m_scales = [torch.ones(b, dtype=torch.float32, **kw) for b in blocks]
-            self.v_scales = [torch.ones(b, dtype=torch.float32, **kw) for b in blocks]
-        self.step_state = torch.zeros(2, dtype=torch.int32, **kw)
+            self.m_scales = [like.new_ones(-(-n // ADAMW_BLOCK), dtype=torch.float32) for n in self._sizes]
+            self.v_scales = [like.new_ones(-(-n // ADAMW_BLOCK), dtype=torch.float32) for n in self._sizes]
+        self.step_state = like.new_zeros(2, dtype=torch.int32)
+
+    def _own(self, column: int, tensors, dtype, sizes) -> tuple:
+        """State tensors of one kind, checked, their addresses put into the table."""
+        tensors = tuple(tensors)
+        for t in tensors:
+            _need(t, dtype, "state")
+        if [t.numel() for t in tensors] != sizes:
+            raise ValueError("a state tensor differs from its parameter in size")
+        _one_device(self.params[0], *tensors)
+        self._table[column::8] = array.array("q", [t.data_ptr() for t in tensors])
+        return tensors
+
+    def _state_dtype(self):
+        return torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
+
+    def _scale_sizes(self):
+        if self.state_bits != 8:
+            raise ValueError("scales go with 8-bit states")
+        return [-(-n // ADAMW_BLOCK) for n in self._sizes]
+
+    m = property(lambda self: self._m)
+    v = property(lambda self: self._v)
+    m_scales = property(lambda self: self._ms)
+    v_scales = property(lambda self: self._vs)
+    _ms = _vs = None
+
+    @m.setter
+    def m(self, tensors):
+        self._m = self._own(2, tensors, self._state_dtype(), self._sizes)
+
+    @v.setter
+    def v(self, tensors):
+        self._v = self._own(3, tensors, self._state_dtype(), self._sizes)
+
+    @m_scales.setter
+    def m_scales(self, tensors):
+        if tensors is not None or self.state_bits == 8:
+            self._ms = self._own(4, tensors, torch.float32, self._scale_sizes())
+
+    @v_scales.setter
+    def v_scales(self, tensors):
+        if tensors is not None or self.state_bits == 8:
+            self._vs = self._own(5, tensors, torch.float32, self._scale_sizes())
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
         """One step with the gradients of params (same order and sizes, all
@@ -867,16 +913,11 @@ class AdamW:
         gd = grads[0].dtype
         if gd not in (torch.float32, torch.bfloat16):
             raise TypeError(f"grads must be float32 or bfloat16, got {gd}")
-        sizes = [p.numel() for p in self.params]
-        for g, n in zip(grads, sizes):
-            if g.dtype is not gd or g.device != self.device or not g.is_contiguous() or g.numel() != n:
+        if (list(map(torch.Tensor.numel, grads)) != self._sizes or not all(map(torch.Tensor.is_contiguous, grads))
+                or any(g.dtype is not gd or g.device != self.device for g in grads)):
+            for g in grads:
                 _need(g, gd, "grads")
-                raise ValueError("a gradient differs from its parameter in size or device")
-        if [p.device for p in self.params] != [self.device] * len(sizes) or not all(p.is_contiguous() for p in self.params):
-            raise ValueError("a parameter has been moved since the optimizer was made")
-        for ts in (self.m, self.v):
-            if [t.numel() for t in ts] != sizes:
-                raise ValueError("a state tensor differs from its parameter in size")
+            raise ValueError("a gradient differs from its parameter in size or device")
         lr_dev = None
         lr = self.lr
         for t, what in ((lr if isinstance(lr, torch.Tensor) else None, "lr"), (grad_scale, "grad_scale")):
@@ -887,14 +928,12 @@ class AdamW:
                 _one_device(self.params[0], t)
         if isinstance(lr, torch.Tensor):
             lr_dev, lr = lr, 0.0
-        none = [0] * len(self.params)
-        eight = self.state_bits == 8
-        ptr = torch.Tensor.data_ptr
-        # entries of sbn_adamw_tensor: eight 64-bit words each
-        words = [x for e in zip(map(ptr, self.params), map(ptr, grads), map(ptr, self.m), map(ptr, self.v),
-                                map(ptr, self.m_scales) if eight else none, map(ptr, self.v_scales) if eight else none,
-                                none if self.copies is None else map(ptr, self.copies), sizes) for x in e]
-        table = array.array("q", words)
+        # the parameters' own storage may have been exchanged since the last step
+        table, ptr = self._table, torch.Tensor.data_ptr
+        table[0::8] = array.array("q", map(ptr, self.params))
+        table[1::8] = array.array("q", map(ptr, grads))
+        if self.copies is not None:
+            table[6::8] = array.array("q", map(ptr, self.copies))
         _run_on(self.device, "sbn_adamw", stream, table.buffer_info()[0], len(self.params),
                 int(self.params[0].dtype == torch.bfloat16), int(gd == torch.bfloat16), self.state_bits,
                 _ptr(self.step_state), float(lr), _ptr(lr_dev), float(self.betas[0]), float(self.betas[1]),
