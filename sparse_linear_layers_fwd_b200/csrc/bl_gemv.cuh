@@ -158,7 +158,7 @@ SBN_DEVFN void gv_codes_eo(uint32_t v, uint32_t& ev, uint32_t& od) {
 // j (the j-th set bit below i), found in ev byte j/2 (even j) or od byte
 // (j-1)/2 (odd j); pruned positions take od byte 3 (code 7), which is zero
 // because a group with a pruned position keeps fewer than 8 codes.
-SBN_DEVFN uint2 gv_selector_pair(uint32_t mask8) {
+SBN_DEVFN uint32_t gv_selector(uint32_t mask8) {
   uint32_t sel = 0u, j = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -167,7 +167,22 @@ SBN_DEVFN uint2 gv_selector_pair(uint32_t mask8) {
     sel |= src << (4 * i);
     j += bit;
   }
+  return sel;
+}
+SBN_DEVFN uint2 gv_selector_pair(uint32_t mask8) {
+  const uint32_t sel = gv_selector(mask8);
   return make_uint2(sel & 0xFFFFu, sel >> 16);
+}
+
+// The two final permutes, from a selector pair or from both halves in a word
+// (half the shared-memory traffic for one shift more).
+SBN_DEVFN void gv_place(const uint2& sel, uint32_t ev, uint32_t od, uint32_t& w0, uint32_t& w1) {
+  w0 = gv_prmt(ev, od, sel.x);
+  w1 = gv_prmt(ev, od, sel.y);
+}
+SBN_DEVFN void gv_place(uint32_t sel, uint32_t ev, uint32_t od, uint32_t& w0, uint32_t& w1) {
+  w0 = gv_prmt(ev, od, sel);
+  w1 = gv_prmt(ev, od, sel >> 16);
 }
 
 // The bits of the word array from bit OFF on, masked with MASK (compile-time
@@ -188,8 +203,8 @@ SBN_DEVFN uint32_t gv_field(const uint32_t (&w)[NW]) {
 // s_sel2: the selector pairs of the 256 keep masks, COPIES of each in a row
 // (a reader with its own copy meets fewer bank conflicts).
 // TABLE: the byte each code becomes (0 for a pruned position).
-template <int MM, int CB, bool DENSE, int I, int COPIES = 1, uint32_t TABLE = kCodeByteTable>
-SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* s_sel2, uint32_t& w0,
+template <int MM, int CB, bool DENSE, int I, int COPIES = 1, uint32_t TABLE = kCodeByteTable, typename Sel = uint2>
+SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const Sel* s_sel2, uint32_t& w0,
                          uint32_t& w1) {
   if constexpr (DENSE) {
     // n == m: 8 codes per group, no keep bits; interleave even and odd
@@ -206,9 +221,7 @@ SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], cons
     const uint32_t m8 = gv_prmt(mw[I / 4], 0u, 0x4440u | (I % 4));
     const uint32_t ev = gv_prmt(TABLE, 0u, gv_field<kOff, kMask, CB>(cw));
     const uint32_t od = gv_prmt(TABLE, 0u, gv_field<kOff + 2, kMask, CB>(cw));
-    const uint2 sel = s_sel2[m8 * COPIES];
-    w0 = gv_prmt(ev, od, sel.x);
-    w1 = gv_prmt(ev, od, sel.y);
+    gv_place(s_sel2[m8 * COPIES], ev, od, w0, w1);
     return;
   } else {
     // m = 16: a 16-position group keeps 4*CB codes, split unevenly between
@@ -225,9 +238,7 @@ SBN_DEVFN void gv_expand(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], cons
     const uint32_t m8 = gv_prmt(mw[I / 4], 0u, 0x4440u | (I % 4));
     uint32_t ev, od;
     gv_codes_eo<TABLE>(v, ev, od);
-    const uint2 sel = s_sel2[m8 * COPIES];
-    w0 = gv_prmt(ev, od, sel.x);
-    w1 = gv_prmt(ev, od, sel.y);
+    gv_place(s_sel2[m8 * COPIES], ev, od, w0, w1);
   }
 }
 

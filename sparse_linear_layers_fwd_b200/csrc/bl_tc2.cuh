@@ -366,11 +366,8 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
           const int tk = tok0 + 32 * c + lane;
           const float sc_next = tk < p.T ? __fdiv_rn(__fmul_rn(g, __ldg(p.xs + tk)), 127.0f) : 0.f;
           epi_chunk(ep, eo, et, tmem + lane_base + (uint32_t)(b * C::BN + 32 * c), sc_next, bias, row_w, tok0 + 32 * c,
-                    p.T, cc + 1 < nch ? tok0 + 32 * (c + 1) : -1, lane, res);
+                    p.T, cc + 1 < nch ? tok0 + 32 * (c + 1) : -1, lane, res, cc + 1 < nch ? nullptr : &acc_empty[b]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[b]);
         continue;
       }
       uint32_t ra[32], rb[32];

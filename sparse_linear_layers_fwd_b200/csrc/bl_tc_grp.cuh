@@ -7,23 +7,23 @@
 // bias_e) + residual. Without offsets it is one layer over all rows.
 //
 // A persistent CTA per SM walks the tiles of the work list (grp.cuh): 128
-// output features x up to 160 rows of one expert, an expert's rows split into
-// equal tiles (of 32-row chunks; the MMA's N is a multiple of 16). The packed weights
-// are read once per tile and expanded on the way to the MMA, since an expert
-// sees few rows: expanding them in memory first would cost as much as the
-// product itself at 500 rows.
+// output features x up to 256 rows of one expert, an expert's rows split into
+// equal tiles (of 32-row chunks; the MMA's N is a multiple of 16). The packed
+// weights are read once per tile and expanded on the way to the MMA, since an
+// expert sees few rows: expanding them in memory first would cost as much as
+// the product itself at 500 rows.
 //
 // The expanded weights go from the producers' registers straight into tensor
 // memory, as the MMA's A operand (lane = feature, 32-bit column = four
 // positions): they never touch shared memory, whose bandwidth the activations
 // need (read by the MMA at 64 bytes a cycle, written by TMA at the same rate).
-//   warp 0      TMA of the activation rows (boxes of 64 and 16 rows), stages of
-//               256 positions;
-//   warp 1      TMEM allocation and the MMA thread;
+//   warp 0      TMA of the activation rows (boxes of 64 and 16 rows), blocks of
+//               128 positions;
+//   warp 1      TMEM allocation and the MMA warp;
 //   warp 2      the work list, then TMA of the packed rows (codes and keep
 //               bits of 128 features x 256 positions) into a ring of their own;
-//   warps 4-15  producers: three groups of four warps, one for each stage of
-//               the ring; a thread expands its feature's 256 positions
+//   warps 4-15  producers: three groups of four warps take stages of 256
+//               positions in turn; a thread expands its feature's positions
 //               (bl_gemv.cuh's expansion), 32 registers per tcgen05.st;
 //   warps 16-23 epilogue (epi_tile.cuh), two per TMEM lane quadrant, the
 //               first taking the first half of a tile's 32-row chunks.
@@ -32,13 +32,12 @@
 // live in uniform registers, and eight MMAs are issued in 190 cycles instead
 // of 840. Every lane waits on a barrier itself, which is faster than one lane
 // and a shuffle.
-// One ring of three stages serves both operands (TMEM: two accumulators of
-// 160 columns, three A slots of 64): one barrier to wait for and one commit
-// per stage, since what the MMA thread does between two stages leaves the
-// tensor pipe idle (with separate rings of three activation stages and two A
-// slots behind 192-column accumulators, 340 of 1070 cycles). Rows of the next
-// expert that share a box are loaded and multiplied, never stored. All waits
-// are bounded in time.
+// TMEM: one accumulator of 256 columns and four A slots of 64. The expansion
+// sets the pace (the integer pipe and shared-memory reads of its selectors), so
+// a wide tile, which expands each weight once per 256 rows, is worth more
+// than a second accumulator behind which the epilogue would hide. Rows of the
+// next expert that share a box are loaded and multiplied, never stored. All
+// waits are bounded in time.
 #pragma once
 
 #include <cuda.h>
@@ -53,26 +52,26 @@
 namespace sbn {
 
 constexpr int kTgBM = 128;
-constexpr int kTgBN = 160;
-constexpr int kTgStages = 3;                   // stages of 256 positions
-constexpr int kTgSub = kTgBN * 128;            // activations of one 128-position block
-constexpr int kTgStageBytes = 2 * kTgSub;
-constexpr uint32_t kTgACol = 2 * kTgBN;        // A slots after the accumulators
-static_assert(kTgACol + 64 * kTgStages <= kTcTmemCols, "accumulators and A slots fit in TMEM");
-static_assert(kTgSub % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
+constexpr int kTgBN = 256;
+constexpr int kTgBlocks = 4;                   // activation ring, blocks of 128 positions
+constexpr int kTgBlockBytes = kTgBN * 128;
+constexpr int kTgSlots = 4;                    // A slots of 256 positions in TMEM
+constexpr uint32_t kTgACol = kTgBN;            // after the accumulator
+static_assert(kTgACol + 64 * kTgSlots <= kTcTmemCols, "accumulator and A slots fit in TMEM");
+constexpr int kTgGroups = 3;                   // of four producer warps
 constexpr int kTgPackedBytes = kTgBM * (48 + 32);   // packed rows of a stage, at most (6:8; n == m: 64 and no keep bits)
-constexpr int kTgPacked = 5;                   // their ring: a slot is free only when its stage is expanded
+constexpr int kTgPacked = 4;                   // their ring: a slot is free only when its stage is expanded
 constexpr int kTgThreads = 768;
 constexpr int kTgEpiWarp = 16;                 // first epilogue warp
-constexpr int kTgSelCopies = 4;
+constexpr int kTgSelCopies = 8;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgYBuf = kTgEpiWarps * (4096 + 128);
-constexpr int kTgBars = 2 * (kTgStages + kTgPacked) + 4;
+constexpr int kTgBars = 2 * (kTgBlocks + kTgSlots + kTgPacked + 1);
 constexpr int kTgList = 64;                    // tiles of a CTA whose place is worked out ahead
 constexpr uint32_t kTgIdesc0 = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTgBM >> 4) << 24);
 
 __host__ __device__ inline size_t tg_smem_bytes(int experts) {
-  return 1024 + (size_t)kTgStages * kTgStageBytes + (size_t)kTgPacked * kTgPackedBytes + kTgYBuf + 256 * 8 * kTgSelCopies +
+  return 1024 + (size_t)kTgBlocks * kTgBlockBytes + (size_t)kTgPacked * kTgPackedBytes + kTgYBuf + 256 * 4 * kTgSelCopies +
          kTgBars * 8 + 16 + 16 * kTgList + 2 * 4 * (size_t)(experts + 1);
 }
 
@@ -154,7 +153,7 @@ SBN_DEVFN void tg_list(int4* list, int len, const int* off, const int* first, co
 
 // 64 positions (one span of bl_gemv.cuh) -> 16 words of int8.
 template <int MM, int CB, bool DENSE>
-SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* sel, uint32_t* w) {
+SBN_DEVFN void tg_expand64(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint32_t* sel, uint32_t* w) {
   gv_expand<MM, CB, DENSE, 0, kTgSelCopies>(cw, mw, sel, w[0], w[1]);
   gv_expand<MM, CB, DENSE, 1, kTgSelCopies>(cw, mw, sel, w[2], w[3]);
   gv_expand<MM, CB, DENSE, 2, kTgSelCopies>(cw, mw, sel, w[4], w[5]);
@@ -173,16 +172,18 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
                  const TgParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* packed = smem + (size_t)kTgStages * kTgStageBytes;
+  uint8_t* packed = smem + (size_t)kTgBlocks * kTgBlockBytes;
   uint8_t* ybuf = packed + kTgPacked * kTgPackedBytes;
-  uint2* s_sel = reinterpret_cast<uint2*>(ybuf + kTgYBuf);   // [256][kTgSelCopies]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
-  uint64_t* empty = full + kTgStages;
-  uint64_t* p_full = empty + kTgStages;
+  uint32_t* s_sel = reinterpret_cast<uint32_t*>(ybuf + kTgYBuf);   // [256][kTgSelCopies]
+  uint64_t* b_full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
+  uint64_t* b_empty = b_full + kTgBlocks;
+  uint64_t* a_full = b_empty + kTgBlocks;
+  uint64_t* a_empty = a_full + kTgSlots;
+  uint64_t* p_full = a_empty + kTgSlots;
   uint64_t* p_empty = p_full + kTgPacked;
-  uint64_t* acc_full = p_empty + kTgPacked;   // [2]
-  uint64_t* acc_empty = acc_full + 2;         // [2]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* acc_full = p_empty + kTgPacked;
+  uint64_t* acc_empty = acc_full + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 1);
   int4* s_list = reinterpret_cast<int4*>(s_tmem + 4);
   int* s_off = reinterpret_cast<int*>(s_list + kTgList);
   int* s_first = s_off + p.grp.experts + 1;
@@ -193,18 +194,20 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   const int row_tiles = (p.N + kTgBM - 1) / kTgBM;
 
   if (tid == 0) {
-    for (int s = 0; s < kTgStages; ++s) {
-      mbar_init(&full[s], 4 + 1);   // the stage's producer warps and the activations' TMA
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < kTgBlocks; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
+    }
+    for (int s = 0; s < kTgSlots; ++s) {
+      mbar_init(&a_full[s], 4);   // a group's warps
+      mbar_init(&a_empty[s], 1);
     }
     for (int s = 0; s < kTgPacked; ++s) {
       mbar_init(&p_full[s], 1);
       mbar_init(&p_empty[s], 4);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kTgEpiWarps);
-    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, kTgEpiWarps);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 0 && lane == 0) {
@@ -221,7 +224,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   if (!DENSE) {
-    for (int i = tid; i < 256 * kTgSelCopies; i += blockDim.x) s_sel[i] = gv_selector_pair((uint32_t)(i / kTgSelCopies));
+    for (int i = tid; i < 256 * kTgSelCopies; i += blockDim.x) s_sel[i] = gv_selector((uint32_t)(i / kTgSelCopies));
   }
   griddep_wait();
   if (warp == 2) grp_build(p.grp, kTgBN, row_tiles, 0, s_off, s_first);
@@ -236,7 +239,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   int used = 0;   // tiles this role has worked on
 
   if (warp == 0) {
-    // ---- TMA of the activation rows (a half stage's second block: zeros) ----
+    // ---- TMA of the activation rows ----
     const bool lead = elect_one();
     int s = 0;
     uint32_t ph = 1;
@@ -245,21 +248,17 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       const int nmma = __shfl_sync(0xffffffffu, t.nmma, 0), tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
-      for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
-        uint8_t* dst = smem + (size_t)s * kTgStageBytes;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait(&b_empty[s], ph)) { ok = false; break; }
+        uint8_t* dst = smem + (size_t)s * kTgBlockBytes;
         if (lead) {
-          mbar_arrive_expect_tx(&full[s], (uint32_t)nmma * 256u);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int x = ks * 256 + j * 128;
-            int r = 0;
-            for (; r + 64 <= nmma; r += 64) tma_load_2d(dst + j * kTgSub + r * 128, &tmap_x64, x, tok0 + r, &full[s]);
-            for (; r < nmma; r += 16) tma_load_2d(dst + j * kTgSub + r * 128, &tmap_x16, x, tok0 + r, &full[s]);
-          }
+          mbar_arrive_expect_tx(&b_full[s], (uint32_t)nmma * 128u);
+          int r = 0;
+          for (; r + 64 <= nmma; r += 64) tma_load_2d(dst + r * 128, &tmap_x64, kb * 128, tok0 + r, &b_full[s]);
+          for (; r < nmma; r += 16) tma_load_2d(dst + r * 128, &tmap_x16, kb * 128, tok0 + r, &b_full[s]);
         }
         __syncwarp();
-        if (++s == kTgStages) {
+        if (++s == kTgBlocks) {
           s = 0;
           ph ^= 1u;
         }
@@ -296,8 +295,8 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     // stay in uniform registers), one elected lane issues ----
     const bool lead = elect_one();
     const uint64_t bdesc0 = sw128_kmajor_desc(smem_u32(smem));
-    int s = 0;
-    uint32_t ph = 0;
+    int s = 0, a = 0;
+    uint32_t ph = 0, pa = 0;
     bool ok = true;
     TgTile t = count ? tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, 0, row_tiles) : TgTile{};
     for (int k = 0; k < count && ok; ++k) {
@@ -305,58 +304,60 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       if (k + 1 < count) t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k + 1, row_tiles);
       if (!nmma) continue;
       const uint32_t idesc = __shfl_sync(0xffffffffu, kTgIdesc0 | ((uint32_t)(nmma >> 3) << 17), 0);
-      const int b = used & 1;
-      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
-      const uint32_t d_tmem = tmem + (uint32_t)(b * kTgBN);
-      for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgStageBytes / 16));
-        const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)s;
-        if (lead) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tc_mma_i8_ta(d_tmem, a_tmem + 8u * (uint32_t)i, bdesc + (uint64_t)(2 * i), idesc, (ks > 0 || i > 0) ? 1u : 0u);
-          if (2 * ks + 1 < nkb) {
+      if (!mbar_wait(acc_empty, (used & 1u) ^ 1u)) break;
+      for (int ks = 0; ks < nst && ok; ++ks) {
+        if (!mbar_wait(&a_full[a], pa)) { ok = false; break; }
+        const int nsub = 2 * ks + 1 < nkb ? 2 : 1;
+        for (int j = 0; j < nsub; ++j) {
+          if (!mbar_wait(&b_full[s], ph)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgBlockBytes / 16));
+          const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)a + 32u * (uint32_t)j;
+          if (lead) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tc_mma_i8_ta(d_tmem, a_tmem + 32u + 8u * (uint32_t)i, bdesc + (uint64_t)(kTgSub / 16 + 2 * i), idesc, 1u);
+              tc_mma_i8_ta(tmem, a_tmem + 8u * (uint32_t)i, bdesc + (uint64_t)(2 * i), idesc,
+                           (ks > 0 || j > 0 || i > 0) ? 1u : 0u);
+            tc_commit(&b_empty[s]);
+            if (j + 1 == nsub) tc_commit(&a_empty[a]);
           }
-          tc_commit(&empty[s]);
+          __syncwarp();
+          if (++s == kTgBlocks) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
-        if (++s == kTgStages) {
-          s = 0;
-          ph ^= 1u;
+        if (++a == kTgSlots) {
+          a = 0;
+          pa ^= 1u;
         }
       }
-      if (lead) tc_commit(&acc_full[b]);
+      if (lead) tc_commit(acc_full);
       __syncwarp();
       ++used;
     }
-    // the last commits before TMEM is freed (also on the abort path)
-    for (int j = used - 2; j < used; ++j)
-      if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
+    // the last commit before TMEM is freed (also on the abort path)
+    if (used) mbar_wait(acc_full, (used - 1) & 1u);
     __syncwarp();
   } else if (warp >= 4 && warp < kTgEpiWarp) {
-    // ---- producers: thread = feature 32 q + lane, group g = stage of the ring
-    // (a half stage's second block: zeros, not multiplied) ----
-    const int q = warp & 3, s = (warp - 4) >> 2;
+    // ---- producers: thread = feature 32 q + lane, group g takes the stages with
+    // index = g (mod 3) over all tiles (a half stage's second block: zeros, not
+    // multiplied) ----
+    const int q = warp & 3, g = (warp - 4) >> 2;
     const int i = 32 * q + lane;
-    const uint2* sel = s_sel + (lane & (kTgSelCopies - 1));
-    const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)s + ((uint32_t)(32 * q) << 16);
+    const uint32_t* sel = s_sel + (lane & (kTgSelCopies - 1));
+    const uint32_t a_base = tmem + kTgACol + ((uint32_t)(32 * q) << 16);
     int it = 0;   // stages over all tiles
-    uint32_t ph = 0;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
       const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
       // this group's stages of the tile
       const int end = it + nst;
-      int mine = it + (s - it % kTgStages + kTgStages) % kTgStages;
+      int mine = it + (g - it % kTgGroups + kTgGroups) % kTgGroups;
       it = end;
-      for (; mine < end; mine += kTgStages, ph ^= 1u) {
-        const int ps = mine % kTgPacked;
+      for (; mine < end; mine += kTgGroups) {
+        const int ps = mine % kTgPacked, s = mine % kTgSlots;
         if (!mbar_wait(&p_full[ps], (mine / kTgPacked) & 1u)) { ok = false; break; }
         const uint2* cp = reinterpret_cast<const uint2*>(packed + ps * kTgPackedBytes + i * 16 * CB);
         const uint4* mp = reinterpret_cast<const uint4*>(packed + ps * kTgPackedBytes + kTgBM * 16 * CB + i * 32);
@@ -376,10 +377,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
           tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
           tg_expand64<MM, CB, DENSE>(cw[1], m1, sel, w + 16);
           if (j == 0) {
-            if (!mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+            if (!mbar_wait(&a_empty[s], ((mine / kTgSlots) & 1u) ^ 1u)) { ok = false; break; }
             tc_fence_after();
           }
-          tmem_st32(a_tmem + 32u * (uint32_t)j, w);
+          tmem_st32(a_base + 64u * (uint32_t)s + 32u * (uint32_t)j, w);
         }
         if (!ok) break;
         tc_fence_before();
@@ -387,7 +388,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         if (lane == 0) {
           // the packed rows only now, when what was loaded of them has been used
           mbar_arrive(&p_empty[ps]);
-          mbar_arrive(&full[s]);
+          mbar_arrive(&a_full[s]);
         }
       }
     }
@@ -402,7 +403,6 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     for (int k = 0; k < count; ++k) {
       const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
-      const int b = used & 1;
       const int row_w = t.row0 + 32 * q;
       const float gm = __ldg(p.gamma + t.e);
       const float bias = (p.ep.bias && row_w + lane < p.N) ? __ldg(p.ep.bias + (size_t)t.e * p.N + row_w + lane) : 0.f;
@@ -412,7 +412,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       uint4 res[4];
       epi_load_residual(p.ep, out, row_w, tok_w, t.tok_end, lane, res);
       float xs_n = tok_w + lane < t.tok_end ? __ldg(p.xs + tok_w + lane) : 0.f;
-      if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
+      if (!mbar_wait(acc_full, used & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1
@@ -420,12 +420,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         const int tok = t.tok0 + 32 * c;
         const float sc = __fdiv_rn(__fmul_rn(gm, xs_n), 127.0f);
         xs_n = tok + 32 + lane < t.tok_end ? __ldg(p.xs + tok + 32 + lane) : 0.f;
-        epi_chunk(p.ep, out, et, tmem + lane_base + (uint32_t)(b * kTgBN + 32 * c), sc, bias, row_w, tok, t.tok_end,
-                  c + 1 < c_end ? tok + 32 : -1, lane, res);
+        epi_chunk(p.ep, out, et, tmem + lane_base + (uint32_t)(32 * c), sc, bias, row_w, tok, t.tok_end,
+                  c + 1 < c_end ? tok + 32 : -1, lane, res, c + 1 < c_end ? nullptr : acc_empty);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (c_first == c_end && lane == 0) mbar_arrive(acc_empty);   // no chunk for this warp
     }
     if (lane == 0) tma_store_wait_all();
     griddep_launch_dependents();

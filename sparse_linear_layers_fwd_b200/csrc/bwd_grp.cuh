@@ -53,7 +53,7 @@
 
 namespace sbn {
 
-constexpr int kGxSelCopies = kTgSelCopies;
+constexpr int kGxSelCopies = 8;
 constexpr int kGxThreads = 768;
 constexpr int kGxEpiWarp = 20;                       // first epilogue warp
 constexpr int kGxPackedBytes = kBxBK * (48 + 32);    // packed rows of a stage, at most (6:8)
@@ -62,13 +62,13 @@ constexpr int kGxList = 32;
 constexpr uint32_t kBf16HighTable = 0xBF003F00u;     // codes 00, 01, 10, 11 -> high byte of bf16
 
 __host__ __device__ inline size_t gx_smem_bytes(int experts) {
-  return 1024 + (size_t)kBxStages * kBxStageBytes + kGxPacked * kGxPackedBytes + 256 * 8 * kGxSelCopies +
+  return 1024 + (size_t)kBxStages * kBxStageBytes + kGxPacked * kGxPackedBytes + 256 * 4 * kGxSelCopies +
          (2 * (kBxStages + kGxPacked) + 4) * 8 + 16 + 16 * kGxList + 2 * 4 * (size_t)(experts + 1);
 }
 
 // Eight positions (group I of the span) -> eight bf16 (0, 1 or -1).
 template <int MM, int CB, bool DENSE, int I>
-SBN_DEVFN uint4 gx_expand8(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint2* sel) {
+SBN_DEVFN uint4 gx_expand8(const uint32_t (&cw)[CB], const uint32_t (&mw)[2], const uint32_t* sel) {
   uint32_t h0, h1;
   gv_expand<MM, CB, DENSE, I, kGxSelCopies, kBf16HighTable>(cw, mw, sel, h0, h1);
   const uint32_t l0 = (h0 << 7) & 0x80808080u, l1 = (h1 << 7) & 0x80808080u;
@@ -93,7 +93,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* packed = smem + (size_t)kBxStages * kBxStageBytes;
-  uint2* s_sel = reinterpret_cast<uint2*>(packed + kGxPacked * kGxPackedBytes);
+  uint32_t* s_sel = reinterpret_cast<uint32_t*>(packed + kGxPacked * kGxPackedBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(s_sel + 256 * kGxSelCopies);
   uint64_t* empty = full + kBxStages;
   uint64_t* p_full = empty + kBxStages;
@@ -131,7 +131,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   if (!DENSE) {
-    for (int i = tid; i < 256 * kGxSelCopies; i += blockDim.x) s_sel[i] = gv_selector_pair((uint32_t)(i / kGxSelCopies));
+    for (int i = tid; i < 256 * kGxSelCopies; i += blockDim.x) s_sel[i] = gv_selector((uint32_t)(i / kGxSelCopies));
   }
   griddep_wait();
   if (warp == 2) grp_build(p.grp, kBxBM, col_tiles, 0, s_off, s_first);
@@ -232,7 +232,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
     // ---- producers: group g takes the stages with index = g (mod 2), counted
     // over all tiles; thread = (feature ol of the stage, span q of 64 positions) ----
     const int g = (warp - 4) >> 3, pi = tid - 128 - 256 * g, ol = pi & 63, q = pi >> 6;
-    const uint2* sel = s_sel + (lane & (kGxSelCopies - 1));
+    const uint32_t* sel = s_sel + (lane & (kGxSelCopies - 1));
     const int r = ol & 7;
     uint8_t* const row0 = smem + kBxABytes + (size_t)(ol >> 3) * 4096 + (size_t)q * 1024 + (size_t)r * 128;
     int it = 0;

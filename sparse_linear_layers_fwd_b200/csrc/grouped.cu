@@ -107,9 +107,9 @@ struct LaunchTc {
     if (p.aligned) {
       const uint64_t pitch = 2 * (uint64_t)f.n_out;
       if (!encode_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.y, f.n_out, f.grp.rows, pitch, 32, 32,
-                     CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                     CU_TENSOR_MAP_SWIZZLE_64B) ||
           (f.ep.z && !encode_2d(&tz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.ep.z, f.n_out, f.grp.rows, pitch, 32, 32,
-                                CU_TENSOR_MAP_SWIZZLE_NONE)))
+                                CU_TENSOR_MAP_SWIZZLE_64B)))
         return SBN_ERR_CUDA;
     }
     // tiles: at most one more than rows / kTgBN per expert, for every block of features

@@ -490,8 +490,8 @@ int tc2_max_pairs() {
 }
 
 // TMA map of the bf16 output [T, N_out] for the pair kernel's tile stores:
-// boxes of 32 tokens x 32 rows.
-bool make_out_tensor_map(CUtensorMap* ty, const uint16_t* y, int t, int n_out) {
+// boxes of 32 tokens x 32 rows (with an epilogue: 64-byte swizzle).
+bool make_out_tensor_map(CUtensorMap* ty, const uint16_t* y, int t, int n_out, bool epi) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t gdim[2] = {(cuuint64_t)n_out, (cuuint64_t)t};
@@ -499,7 +499,7 @@ bool make_out_tensor_map(CUtensorMap* ty, const uint16_t* y, int t, int n_out) {
   cuuint32_t box[2] = {32, 32};
   cuuint32_t estride[2] = {1, 1};
   return enc(ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(y), gdim, gstride, box, estride,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, epi ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -510,8 +510,8 @@ sbn_status launch_tc2(const CUtensorMap& tm, const CUtensorMap& tw, const CUtens
   // tile stores of the output where every row starts on a 16-byte boundary
   const bool al = !ACC && p.y && (p.N % 8) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
   CUtensorMap ty = tm, tz = tm;   // unused unless y_tma (tz: and z is wanted)
-  const int y_tma = (al && make_out_tensor_map(&ty, p.y, p.T, p.N) &&
-                     (!EPI || !ep.z || make_out_tensor_map(&tz, ep.z, p.T, p.N))) ? 1 : 0;
+  const int y_tma = (al && make_out_tensor_map(&ty, p.y, p.T, p.N, EPI) &&
+                     (!EPI || !ep.z || make_out_tensor_map(&tz, ep.z, p.T, p.N, EPI))) ? 1 : 0;
   const int tiles = ((p.N + 255) / 256) * ((p.T + C::BN - 1) / C::BN);
   return launch_ex(bl_tc2_kernel<SPARSE, ACC, NARROW, EPI>, dim3(2 * std::min(tiles, max_pairs)), dim3(kT2Threads),
                    C::SMEM, st, 2, tm, tw, te, ty, p, y_tma, tz, ep);
