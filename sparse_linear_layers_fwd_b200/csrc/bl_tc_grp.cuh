@@ -7,7 +7,7 @@
 // bias_e) + residual. Without offsets it is one layer over all rows.
 //
 // A persistent CTA per SM walks the tiles of the work list (grp.cuh): 128
-// output features x up to 256 rows of one expert, an expert's rows split into
+// output features x up to 192 rows of one expert, an expert's rows split into
 // equal tiles (of 32-row chunks; the MMA's N is a multiple of 16). The packed
 // weights are read once per tile and expanded on the way to the MMA, since an
 // expert sees few rows: expanding them in memory first would cost as much as
@@ -22,9 +22,11 @@
 //   warp 1      TMEM allocation and the MMA warp;
 //   warp 2      the work list, then TMA of the packed rows (codes and keep
 //               bits of 128 features x 256 positions) into a ring of their own;
-//   warps 4-15  producers: three groups of four warps take stages of 256
-//               positions in turn; a thread expands its feature's positions
-//               (bl_gemv.cuh's expansion), 32 registers per tcgen05.st;
+//   warps 4-15  producers: three groups of four warps, one for each A slot,
+//               take the 128-position blocks in turn; a thread expands its
+//               feature's positions (bl_gemv.cuh's expansion) into 32 registers
+//               and stores them with tcgen05.st. A slot belongs to one group, so
+//               that a wait by parity can never be two rounds behind or ahead;
 //   warps 16-23 epilogue (epi_tile.cuh), two per TMEM lane quadrant, the
 //               first taking the first half of a tile's 32-row chunks.
 // The loops of the MMA and TMA warps are run by whole warps and only the
@@ -32,12 +34,24 @@
 // live in uniform registers, and eight MMAs are issued in 190 cycles instead
 // of 840. Every lane waits on a barrier itself, which is faster than one lane
 // and a shuffle.
-// TMEM: one accumulator of 256 columns and four A slots of 64. The expansion
-// sets the pace (the integer pipe and shared-memory reads of its selectors), so
-// a wide tile, which expands each weight once per 256 rows, is worth more
-// than a second accumulator behind which the epilogue would hide. Rows of the
-// next expert that share a box are loaded and multiplied, never stored. All
-// waits are bounded in time.
+// TMEM: two accumulators of 192 columns, so that the epilogue hides behind the
+// next tile, and three A slots of 32 columns (a 128-position block each).
+// Measured at 16384 rows (30 of 32 experts, K = 2048, N_out = 2816, 6:8, with the
+// quantization) and at 256 rows of 64 experts (K = 2048, N_out = 1408, 2:4):
+//   this split                                                139 us, 42.7 us
+//   160-column accumulators, one ring of three 256-position
+//   stages for both operands                                  153 us, 39 us
+//   one accumulator of 256 columns, its epilogue exposed      150 us, 43.6 us
+//   four groups of producers and slots (72 registers)         142 us, 42 us
+// What bounds it: a block costs 760 to 1040 cycles, of which the MMAs need 384
+// at 192 rows. Half of the issue slots are taken (the expansion's permutes and
+// the epilogue share the integer pipe, 56 % busy), so that the MMA warp's own
+// instructions wait for theirs: a barrier that is already complete costs it
+// 130 cycles, four MMAs and their commits 210 to 260. A first look at the next
+// block's barriers ahead of the MMAs, deeper rings and wider boxes of packed
+// rows changed nothing.
+// Rows of the next expert that share a box are loaded and multiplied, never
+// stored. All waits are bounded in time.
 #pragma once
 
 #include <cuda.h>
@@ -52,27 +66,28 @@
 namespace sbn {
 
 constexpr int kTgBM = 128;
-constexpr int kTgBN = 256;
-constexpr int kTgBlocks = 4;                   // activation ring, blocks of 128 positions
+constexpr int kTgBN = 192;
+constexpr int kTgBlocks = 5;                   // activation ring, blocks of 128 positions
 constexpr int kTgBlockBytes = kTgBN * 128;
-constexpr int kTgSlots = 4;                    // A slots of 256 positions in TMEM
-constexpr uint32_t kTgACol = kTgBN;            // after the accumulator
-static_assert(kTgACol + 64 * kTgSlots <= kTcTmemCols, "accumulator and A slots fit in TMEM");
-constexpr int kTgGroups = 3;                   // of four producer warps
-constexpr int kTgPackedBytes = kTgBM * (48 + 32);   // packed rows of a stage, at most (6:8; n == m: 64 and no keep bits)
-constexpr int kTgPacked = 4;                   // their ring: a slot is free only when its stage is expanded
+constexpr int kTgSlots = 3;                    // A slots in TMEM, a block and a producer group each
+constexpr uint32_t kTgACol = 2 * kTgBN;        // after the accumulators
+static_assert(kTgACol + 32 * kTgSlots <= kTcTmemCols, "accumulators and A slots fit in TMEM");
+static_assert(kTgBlockBytes % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
+constexpr int kTgSpan = 2;                     // blocks of a stage of packed rows
+constexpr int kTgPackedBytes = kTgBM * (24 + 16) * kTgSpan;   // a stage, at most (6:8; n == m: 32 and no keep bits)
+constexpr int kTgPacked = 5;                   // their ring: a slot is free only when its stage is expanded
 constexpr int kTgThreads = 768;
 constexpr int kTgEpiWarp = 16;                 // first epilogue warp
 constexpr int kTgSelCopies = 8;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgYBuf = kTgEpiWarps * (4096 + 128);
-constexpr int kTgBars = 2 * (kTgBlocks + kTgSlots + kTgPacked + 1);
+constexpr int kTgBars = 2 * (kTgBlocks + kTgSlots + 2) + 3 * kTgPacked;
 constexpr int kTgList = 64;                    // tiles of a CTA whose place is worked out ahead
 constexpr uint32_t kTgIdesc0 = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTgBM >> 4) << 24);
 
 __host__ __device__ inline size_t tg_smem_bytes(int experts) {
   return 1024 + (size_t)kTgBlocks * kTgBlockBytes + (size_t)kTgPacked * kTgPackedBytes + kTgYBuf + 256 * 4 * kTgSelCopies +
-         kTgBars * 8 + 16 + 16 * kTgList + 2 * 4 * (size_t)(experts + 1);
+         16 * kTgList + kTgBars * 8 + 4 + 2 * 4 * (size_t)(experts + 1);
 }
 
 struct TgParams {
@@ -118,18 +133,16 @@ SBN_DEVFN void tc_mma_i8_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, ui
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(0u)
       : "memory");
 }
-// 32 columns of this warp's 32 lanes from registers, and the wait for them.
-SBN_DEVFN void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 16 columns of this warp's 32 lanes from registers, and the wait for all such.
+SBN_DEVFN void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
+SBN_DEVFN void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // The k-th tile of this CTA: from the list (`len` entries), worked out on the
 // spot behind it. BM, BN, STEP: tg_tile's.
@@ -175,22 +188,22 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   uint8_t* packed = smem + (size_t)kTgBlocks * kTgBlockBytes;
   uint8_t* ybuf = packed + kTgPacked * kTgPackedBytes;
   uint32_t* s_sel = reinterpret_cast<uint32_t*>(ybuf + kTgYBuf);   // [256][kTgSelCopies]
-  uint64_t* b_full = reinterpret_cast<uint64_t*>(s_sel + 256 * kTgSelCopies);
+  int4* s_list = reinterpret_cast<int4*>(s_sel + 256 * kTgSelCopies);
+  uint64_t* b_full = reinterpret_cast<uint64_t*>(s_list + kTgList);
   uint64_t* b_empty = b_full + kTgBlocks;
   uint64_t* a_full = b_empty + kTgBlocks;
   uint64_t* a_empty = a_full + kTgSlots;
   uint64_t* p_full = a_empty + kTgSlots;
-  uint64_t* p_empty = p_full + kTgPacked;
+  uint64_t* p_empty = p_full + 2 * kTgPacked;
   uint64_t* acc_full = p_empty + kTgPacked;
-  uint64_t* acc_empty = acc_full + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 1);
-  int4* s_list = reinterpret_cast<int4*>(s_tmem + 4);
-  int* s_off = reinterpret_cast<int*>(s_list + kTgList);
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  int* s_off = reinterpret_cast<int*>(s_tmem + 1);
   int* s_first = s_off + p.grp.experts + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nkb = p.K / 128;            // 128-position blocks
-  const int nst = (nkb + 1) / 2;        // stages of 256 positions
+  const int nst = (nkb + kTgSpan - 1) / kTgSpan;   // stages of packed rows
   const int row_tiles = (p.N + kTgBM - 1) / kTgBM;
 
   if (tid == 0) {
@@ -204,10 +217,13 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     }
     for (int s = 0; s < kTgPacked; ++s) {
       mbar_init(&p_full[s], 1);
-      mbar_init(&p_empty[s], 4);
+      mbar_init(&p_full[s + kTgPacked], 1);
+      mbar_init(&p_empty[s], 4 * kTgSpan);   // the warps of a stage's blocks
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, kTgEpiWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kTgEpiWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 0 && lane == 0) {
@@ -267,7 +283,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
   } else if (warp == 2) {
     // ---- TMA of the packed rows ----
     const bool lead = elect_one();
-    int s = 0;
+    int s = 0, f = 0;   // slot, and barrier of its arrival
     uint32_t ph = 1;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
@@ -279,11 +295,12 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         if (!mbar_wait(&p_empty[s], ph)) { ok = false; break; }
         uint8_t* dst = packed + s * kTgPackedBytes;
         if (lead) {
-          mbar_arrive_expect_tx(&p_full[s], (uint32_t)(kTgBM * (16 * CB + (DENSE ? 0 : 32))));
-          tma_load_2d(dst, &tmap_c, ks * 16 * CB, row, &p_full[s]);
-          if (!DENSE) tma_load_2d(dst + kTgBM * 16 * CB, &tmap_m, ks * 32, row, &p_full[s]);
+          mbar_arrive_expect_tx(&p_full[f], (uint32_t)(kTgBM * kTgSpan * (8 * CB + (DENSE ? 0 : 16))));
+          tma_load_2d(dst, &tmap_c, ks * 16 * CB, row, &p_full[f]);
+          if (!DENSE) tma_load_2d(dst + kTgBM * kTgSpan * 8 * CB, &tmap_m, ks * kTgSpan * 16, row, &p_full[f]);
         }
         __syncwarp();
+        if (++f == 2 * kTgPacked) f = 0;
         if (++s == kTgPacked) {
           s = 0;
           ph ^= 1u;
@@ -304,93 +321,91 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       if (k + 1 < count) t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k + 1, row_tiles);
       if (!nmma) continue;
       const uint32_t idesc = __shfl_sync(0xffffffffu, kTgIdesc0 | ((uint32_t)(nmma >> 3) << 17), 0);
-      if (!mbar_wait(acc_empty, (used & 1u) ^ 1u)) break;
-      for (int ks = 0; ks < nst && ok; ++ks) {
-        if (!mbar_wait(&a_full[a], pa)) { ok = false; break; }
-        const int nsub = 2 * ks + 1 < nkb ? 2 : 1;
-        for (int j = 0; j < nsub; ++j) {
-          if (!mbar_wait(&b_full[s], ph)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgBlockBytes / 16));
-          const uint32_t a_tmem = tmem + kTgACol + 64u * (uint32_t)a + 32u * (uint32_t)j;
-          if (lead) {
+      const int b = used & 1;
+      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      const uint32_t d_tmem = tmem + (uint32_t)(b * kTgBN);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait(&b_full[s], ph) || !mbar_wait(&a_full[a], pa)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgBlockBytes / 16));
+        const uint32_t a_tmem = tmem + kTgACol + 32u * (uint32_t)a;
+        if (lead) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              tc_mma_i8_ta(tmem, a_tmem + 8u * (uint32_t)i, bdesc + (uint64_t)(2 * i), idesc,
-                           (ks > 0 || j > 0 || i > 0) ? 1u : 0u);
-            tc_commit(&b_empty[s]);
-            if (j + 1 == nsub) tc_commit(&a_empty[a]);
-          }
-          __syncwarp();
-          if (++s == kTgBlocks) {
-            s = 0;
-            ph ^= 1u;
-          }
+          for (int i = 0; i < 4; ++i)
+            tc_mma_i8_ta(d_tmem, a_tmem + 8u * (uint32_t)i, bdesc + (uint64_t)(2 * i), idesc,
+                         (kb > 0 || i > 0) ? 1u : 0u);
+          tc_commit(&a_empty[a]);
+          tc_commit(&b_empty[s]);
+        }
+        __syncwarp();
+        if (++s == kTgBlocks) {
+          s = 0;
+          ph ^= 1u;
         }
         if (++a == kTgSlots) {
           a = 0;
           pa ^= 1u;
         }
       }
-      if (lead) tc_commit(acc_full);
+      if (lead) tc_commit(&acc_full[b]);
       __syncwarp();
       ++used;
     }
-    // the last commit before TMEM is freed (also on the abort path)
-    if (used) mbar_wait(acc_full, (used - 1) & 1u);
+    // the last commits before TMEM is freed (also on the abort path)
+    for (int j = used - 2; j < used; ++j)
+      if (j >= 0) mbar_wait(&acc_full[j & 1], (j >> 1) & 1u);
     __syncwarp();
   } else if (warp >= 4 && warp < kTgEpiWarp) {
-    // ---- producers: thread = feature 32 q + lane, group g takes the stages with
-    // index = g (mod 3) over all tiles (a half stage's second block: zeros, not
-    // multiplied) ----
+    // ---- producers: thread = feature 32 q + lane, group g takes the blocks with
+    // index = g (mod 3) over all tiles, into slot g ----
     const int q = warp & 3, g = (warp - 4) >> 2;
     const int i = 32 * q + lane;
     const uint32_t* sel = s_sel + (lane & (kTgSelCopies - 1));
-    const uint32_t a_base = tmem + kTgACol + ((uint32_t)(32 * q) << 16);
-    int it = 0;   // stages over all tiles
+    const uint32_t a_tmem = tmem + kTgACol + 32u * (uint32_t)g + ((uint32_t)(32 * q) << 16);
+    int it = 0, blk = 0;   // stages and blocks before the tile
+    uint32_t ph = 1u;
     bool ok = true;
     for (int k = 0; k < count && ok; ++k) {
       const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
-      // this group's stages of the tile
-      const int end = it + nst;
-      int mine = it + (g - it % kTgGroups + kTgGroups) % kTgGroups;
-      it = end;
-      for (; mine < end; mine += kTgGroups) {
-        const int ps = mine % kTgPacked, s = mine % kTgSlots;
-        if (!mbar_wait(&p_full[ps], (mine / kTgPacked) & 1u)) { ok = false; break; }
-        const uint2* cp = reinterpret_cast<const uint2*>(packed + ps * kTgPackedBytes + i * 16 * CB);
-        const uint4* mp = reinterpret_cast<const uint4*>(packed + ps * kTgPackedBytes + kTgBM * 16 * CB + i * 32);
-#pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-          uint32_t cw[2][CB];
+      for (int kb = (g - blk % kTgSlots + kTgSlots) % kTgSlots; kb < nkb; kb += kTgSlots, ph ^= 1u) {
+        // Two arrival barriers for a packed slot, taken in turn: a group may look
+        // before the slot's previous stage has landed, but never before the one
+        // before that (it has seen the MMA of the block 2 kTgSlots back).
+        const int st = it + kb / kTgSpan, ps = st % kTgPacked, j = kb % kTgSpan;
+        if (!mbar_wait(&p_full[st % (2 * kTgPacked)], (uint32_t)(st / (2 * kTgPacked)) & 1u)) { ok = false; break; }
+        const uint2* cp = reinterpret_cast<const uint2*>(packed + ps * kTgPackedBytes + (i * kTgSpan + j) * 8 * CB);
+        uint32_t cw[2][CB];
 #pragma unroll
-          for (int h = 0; h < CB; ++h) {
-            const uint2 c2 = cp[CB * j + h];
-            cw[2 * h / CB][2 * h % CB] = c2.x;
-            cw[(2 * h + 1) / CB][(2 * h + 1) % CB] = c2.y;
-          }
-          uint4 mv = make_uint4(0u, 0u, 0u, 0u);
-          if (!DENSE) mv = mp[j];
-          const uint32_t m0[2] = {mv.x, mv.y}, m1[2] = {mv.z, mv.w};
-          uint32_t w[32];
-          tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
-          tg_expand64<MM, CB, DENSE>(cw[1], m1, sel, w + 16);
-          if (j == 0) {
-            if (!mbar_wait(&a_empty[s], ((mine / kTgSlots) & 1u) ^ 1u)) { ok = false; break; }
-            tc_fence_after();
-          }
-          tmem_st32(a_base + 64u * (uint32_t)s + 32u * (uint32_t)j, w);
+        for (int h = 0; h < CB; ++h) {
+          const uint2 c2 = cp[h];
+          cw[2 * h / CB][2 * h % CB] = c2.x;
+          cw[(2 * h + 1) / CB][(2 * h + 1) % CB] = c2.y;
         }
-        if (!ok) break;
+        uint4 mv = make_uint4(0u, 0u, 0u, 0u);
+        if (!DENSE)
+          mv = *reinterpret_cast<const uint4*>(packed + ps * kTgPackedBytes + kTgBM * kTgSpan * 8 * CB + (i * kTgSpan + j) * 16);
+        const uint32_t m0[2] = {mv.x, mv.y}, m1[2] = {mv.z, mv.w};
+        uint32_t w[16], v[16];
+        tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
+        tg_expand64<MM, CB, DENSE>(cw[1], m1, sel, v);
+        if (!mbar_wait(&a_empty[g], ph)) { ok = false; break; }
+        tc_fence_after();
+        tmem_st16(a_tmem, w);
+        tmem_st16(a_tmem + 16u, v);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          // the packed rows only now, when what was loaded of them has been used
-          mbar_arrive(&p_empty[ps]);
-          mbar_arrive(&a_full[s]);
+          mbar_arrive(&a_full[g]);
+          // the packed rows only now, when what was loaded of them has been used:
+          // handed back right behind the loads, they were overwritten before every
+          // lane's loads had been done. The last block counts for those behind it.
+          for (int n = kb + 1 == nkb ? j : kTgSpan - 1; n < kTgSpan; ++n) mbar_arrive(&p_empty[ps]);
         }
       }
+      it += nst;
+      blk += nkb;
     }
   } else if (warp >= kTgEpiWarp) {
     // ---- epilogue ----
@@ -403,6 +418,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
     for (int k = 0; k < count; ++k) {
       const TgTile t = tg_get<kTgBM, kTgBN, 16>(s_list, kTgList, s_off, s_first, p.grp, k, row_tiles);
       if (!t.nmma) continue;
+      const int b = used & 1;
       const int row_w = t.row0 + 32 * q;
       const float gm = __ldg(p.gamma + t.e);
       const float bias = (p.ep.bias && row_w + lane < p.N) ? __ldg(p.ep.bias + (size_t)t.e * p.N + row_w + lane) : 0.f;
@@ -412,7 +428,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       uint4 res[4];
       epi_load_residual(p.ep, out, row_w, tok_w, t.tok_end, lane, res);
       float xs_n = tok_w + lane < t.tok_end ? __ldg(p.xs + tok_w + lane) : 0.f;
-      if (!mbar_wait(acc_full, used & 1u)) break;
+      if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1
@@ -420,10 +436,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         const int tok = t.tok0 + 32 * c;
         const float sc = __fdiv_rn(__fmul_rn(gm, xs_n), 127.0f);
         xs_n = tok + 32 + lane < t.tok_end ? __ldg(p.xs + tok + 32 + lane) : 0.f;
-        epi_chunk(p.ep, out, et, tmem + lane_base + (uint32_t)(32 * c), sc, bias, row_w, tok, t.tok_end,
-                  c + 1 < c_end ? tok + 32 : -1, lane, res, c + 1 < c_end ? nullptr : acc_empty);
+        epi_chunk(p.ep, out, et, tmem + lane_base + (uint32_t)(b * kTgBN + 32 * c), sc, bias, row_w, tok, t.tok_end,
+                  c + 1 < c_end ? tok + 32 : -1, lane, res, c + 1 < c_end ? nullptr : &acc_empty[b]);
       }
-      if (c_first == c_end && lane == 0) mbar_arrive(acc_empty);   // no chunk for this warp
+      if (c_first == c_end && lane == 0) mbar_arrive(&acc_empty[b]);   // no chunk for this warp
     }
     if (lane == 0) tma_store_wait_all();
     griddep_launch_dependents();

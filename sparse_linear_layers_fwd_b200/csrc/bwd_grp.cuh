@@ -53,11 +53,12 @@
 
 namespace sbn {
 
-constexpr int kGxSelCopies = 8;
+constexpr int kGxSelCopies = 4;
 constexpr int kGxThreads = 768;
 constexpr int kGxEpiWarp = 20;                       // first epilogue warp
 constexpr int kGxPackedBytes = kBxBK * (48 + 32);    // packed rows of a stage, at most (6:8)
-constexpr int kGxPacked = 3;                         // their ring
+constexpr int kGxPacked = 4;                         // their ring; even, so that a slot stays with one group and
+                                                     // its parity waits never span two rounds
 constexpr int kGxList = 32;
 constexpr uint32_t kBf16HighTable = 0xBF003F00u;     // codes 00, 01, 10, 11 -> high byte of bf16
 

@@ -42,10 +42,13 @@ SBN_DEVFN int warp_scan_add(int v, int lane) {
 SBN_DEVFN void grp_build(const GrpParams& p, int tile_rows, int per_row_tile, int empty_tiles, int* off, int* first) {
   const int lane = threadIdx.x & 31;
   int top = 0, tiles = 0;   // carried: largest offset so far, tiles so far
+  // an entry's raw offset, loaded a round ahead
+  auto load = [&](int e) { return p.offsets && e <= p.experts ? p.offsets[e] : e >= p.experts ? p.rows : 0; };
+  int next = load(lane);
   for (int e0 = 0; e0 <= p.experts; e0 += 32) {
     const int e = e0 + lane;
-    int v = e >= p.experts ? p.rows : 0;
-    if (p.offsets && e <= p.experts) v = min(max(p.offsets[e], 0), p.rows);
+    int v = min(max(next, 0), p.rows);
+    next = load(e + 32);
     v = max(warp_scan_max(v, lane), top);
     const int prev = __shfl_up_sync(0xffffffffu, v, 1);
     const int before = lane ? prev : top;   // offset of expert e - 1's first row
