@@ -490,12 +490,13 @@ constexpr int kGwStages = 4;
 constexpr int kGwABytes = kGwBM * kGwBK * 2;     // 16 KB
 constexpr int kGwStageBytes = kGwABytes + kGwBN * kGwBK * 2;
 constexpr int kGwThreads = 384;                  // TMA, MMA, list, -, eight epilogue warps
+constexpr int kGwOut = 8 * 2048;                 // a warp's 32 features x 32 positions of dW
 // instruction descriptor: f32 accumulate, fp16 A and B, both MN-major
 constexpr uint32_t kGwIdesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(kGwBN >> 3) << 17) |
                               ((uint32_t)(kGwBM >> 4) << 24);
 
 __host__ __device__ inline size_t gw_smem_bytes(int experts) {
-  return 1024 + (size_t)kGwStages * kGwStageBytes + (2 * kGwStages + 4) * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
+  return 1024 + (size_t)kGwStages * kGwStageBytes + kGwOut + (2 * kGwStages + 4) * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
 }
 
 SBN_DEVFN void tc_mma_f16_gw(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
@@ -506,13 +507,15 @@ SBN_DEVFN void tc_mma_f16_gw(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, ui
       : "memory");
 }
 
-// tmap_a, tmap_x: the fp16 operands, boxes of 64 columns x 64 rows (128-byte swizzle).
+// tmap_a, tmap_x: the fp16 operands, boxes of 64 columns x 64 rows (128-byte swizzle);
+// tmap_dw: dW as [E N, K], boxes of 32 positions x 32 features (64-byte swizzle).
 static __global__ void __launch_bounds__(kGwThreads, 1)
 bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_x,
-                  const GwParams p) {
+                  const __grid_constant__ CUtensorMap tmap_dw, const GwParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kGwStages * kGwStageBytes);
+  uint8_t* out = smem + (size_t)kGwStages * kGwStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out + kGwOut);
   uint64_t* empty = full + kGwStages;
   uint64_t* acc_full = empty + kGwStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;       // [2]
@@ -634,6 +637,8 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         tc_fence_after();
       }
       uint16_t* drow = p.dw + ((size_t)e * p.N + o) * p.K;
+      const int o_w = o - lane;
+      uint8_t* tile_w = out + (warp - 4) * 2048;
 #pragma unroll 1
       for (int c = 4 * half; c < 4 * half + 4; ++c) {
         uint32_t r[32];
@@ -644,12 +649,23 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           for (int i = 0; i < 32; ++i) r[i] = 0u;
         }
         const int kc = k0 + 32 * c;
-        if (o < p.N && kc < p.K) {
-          uint32_t o16[16];
+        uint32_t o16[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o16[i] = (uint32_t)f32_to_bf16_bits(__fmul_rn(sc, __uint_as_float(r[2 * i]))) |
-                     ((uint32_t)f32_to_bf16_bits(__fmul_rn(sc, __uint_as_float(r[2 * i + 1]))) << 16);
+        for (int i = 0; i < 16; ++i)
+          o16[i] = (uint32_t)f32_to_bf16_bits(__fmul_rn(sc, __uint_as_float(r[2 * i]))) |
+                   ((uint32_t)f32_to_bf16_bits(__fmul_rn(sc, __uint_as_float(r[2 * i + 1]))) << 16);
+        if (o_w + 32 <= p.N && kc < p.K) {
+          // through shared memory, so that whole rows of a box leave at once
+          if (lane == 0) tma_store_wait_read0();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(tile_w + epi_piece(lane, i)) =
+                make_uint4(o16[4 * i], o16[4 * i + 1], o16[4 * i + 2], o16[4 * i + 3]);
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&tmap_dw, kc, e * p.N + o_w, tile_w);
+        } else if (o < p.N && kc < p.K) {   // the last features, whose box would reach into the next expert
           uint4* dst = reinterpret_cast<uint4*>(drow + kc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_uint4(o16[4 * i], o16[4 * i + 1], o16[4 * i + 2], o16[4 * i + 3]);
@@ -661,6 +677,7 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         if (lane == 0) mbar_arrive(&acc_empty[b]);
       }
     }
+    if (lane == 0) tma_store_wait_all();
     griddep_launch_dependents();
   }
 

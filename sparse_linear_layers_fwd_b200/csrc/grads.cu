@@ -137,18 +137,20 @@ sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, c
   const unsigned grid = (unsigned)((p.a_ctas + x_ctas + p.cluster - 1) / p.cluster * p.cluster);
   if ((st = launch_ex(bwd_dw_prep_kernel, dim3(grid), dim3(kGpThreads), list, cs, (unsigned)p.cluster, p)) != SBN_OK)
     return st;
-  CUtensorMap ta, tx;
+  CUtensorMap ta, tx, tdw;
   if (!encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.a16, n_out, l.rows, 2 * (uint64_t)n_out, 64, kGwBK,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.x16, k, l.rows, 2 * (uint64_t)k, 64, kGwBK,
-                 CU_TENSOR_MAP_SWIZZLE_128B))
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tdw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.dw, k, (uint64_t)experts * (uint64_t)n_out,
+                 2 * (uint64_t)k, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SBN_ERR_CUDA;
   static bool attr_set[kMaxDevices] = {};
   if (!set_smem_attr_once(bwd_dw_grp_kernel, gw_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
   const long long tiles = (long long)experts * ((n_out + kGwBM - 1) / kGwBM) * ((k + kGwBN - 1) / kGwBN);
   const int main_grid = (int)std::min(tiles, (long long)sms);
   return launch_ex(bwd_dw_grp_kernel, dim3((unsigned)main_grid), dim3(kGwThreads), gw_smem_bytes(experts), cs, 1, ta, tx,
-                   p);
+                   tdw, p);
 }
 
 }  // extern "C"
