@@ -500,12 +500,14 @@ sbn_status sbn_act_grad(const void* dy_bf16, const void* z_bf16, int32_t rows,
  *            aligned, sbn_bitlinear_grouped_x_workspace_bytes) may be NULL when
  *            both are given or rows <= 16 fit the one-kernel route.
  * 1 <= experts <= 1024; shapes as sbn_bitlinear with t = rows.
- * sbn_bitlinear_grouped_grad_x: dX_r = dY_r (gamma_e C_e), [rows, k] bf16.
+ * sbn_bitlinear_grouped_grad_x: dX_r = dY_r (gamma_e C_e), [rows, k] bf16. Its
+ * workspace (16-byte aligned, sbn_bitlinear_grouped_grad_x_workspace_bytes; 0
+ * bytes and NULL for n_out a multiple of 8) holds dY at a pitch of 16 bytes.
  * sbn_bitlinear_grouped_grad_w: dW_e = sum over e's rows of dY_r^T (Xq_r s_r /
  * 127), [experts, n_out, k] bf16, zero for an expert without rows. Its workspace
- * (16-byte aligned, sbn_bitlinear_grouped_grad_w_workspace_bytes; 0 bytes and
- * NULL for n_out not a multiple of 8) holds dY s / 127, scaled by a power of two
- * per expert and feature, and Xq as fp16 (11 bits of every term); fp32 sums.
+ * (16-byte aligned, sbn_bitlinear_grouped_grad_w_workspace_bytes) holds dY s /
+ * 127, scaled by a power of two per expert and feature, and Xq as fp16 (11 bits
+ * of every term); fp32 sums.
  * Errors: SBN_ERR_NULL, SBN_ERR_SHAPE, SBN_ERR_PATTERN, SBN_ERR_ALIGN,
  * SBN_ERR_WORKSPACE (before anything is enqueued); SBN_ERR_CUDA.
  */
@@ -529,7 +531,10 @@ sbn_status sbn_bitlinear_grouped_grad_x(const void* dy_bf16, int32_t rows,
                                         const int32_t* offsets, int32_t experts,
                                         int32_t k, int32_t n_out, int32_t n, int32_t m,
                                         const uint8_t* codes, const uint8_t* meta,
-                                        const float* gamma, void* dx_bf16, void* stream);
+                                        const float* gamma, void* dx_bf16,
+                                        void* workspace, size_t ws_bytes,
+                                        void* stream);
+size_t sbn_bitlinear_grouped_grad_x_workspace_bytes(int32_t rows, int32_t n_out);
 sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq,
                                         const float* x_scale, int32_t rows,
                                         const int32_t* offsets, int32_t experts,

@@ -321,6 +321,38 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
   }
 }
 
+// Eight columns of a row of dY; WHOLE: its rows start on 16-byte boundaries
+// (N_out a multiple of 8), otherwise columns past the last are zeros.
+template <bool WHOLE>
+SBN_DEVFN uint4 gw_load8(const uint16_t* dy, size_t row, int N, int col) {
+  if constexpr (WHOLE) {
+    return __ldg(reinterpret_cast<const uint4*>(dy + row * N + col));
+  } else {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = col + i < N ? __ldg(dy + row * N + col + i) : 0u;
+    return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  }
+}
+
+// dY for dX where N_out is not a multiple of 8: rows copied to a pitch of
+// round_up(N_out, 8), which TMA can load. Bound by DRAM and L2, 4 bytes per
+// element; the alternative, 2-byte loads in the product's own warps, would repeat
+// them for every 256 positions of K.
+constexpr int kGcThreads = 256;
+static __global__ void __launch_bounds__(kGcThreads)
+bwd_pitch_kernel(const uint16_t* __restrict__ dy, uint16_t* __restrict__ dst, int rows, int N) {
+  griddep_wait();
+  const int per_row = (N + 7) / 8;
+  const long long n = (long long)rows * per_row;
+  for (long long i = (long long)blockIdx.x * kGcThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kGcThreads) {
+    const long long row = i / per_row;
+    const int c = (int)(i - row * per_row);
+    reinterpret_cast<uint4*>(dst)[i] = gw_load8<false>(dy, (size_t)row, N, 8 * c);
+  }
+  griddep_launch_dependents();
+}
+
 struct GwParams {
   const uint16_t* dy;
   const int8_t* xq;
@@ -328,7 +360,8 @@ struct GwParams {
   uint16_t* dw;     // [E, N, K]
   GrpParams grp;
   int K, N;
-  // workspace: fp16 [padded rows, N] and [padded rows, K], and the factor
+  int Np;           // N rounded up to a multiple of 8
+  // workspace: fp16 [padded rows, Np] and [padded rows, K], and the factor
   // that undoes the scaling of a, [E, N]
   uint16_t* a16;
   uint16_t* x16;
@@ -350,7 +383,8 @@ constexpr int kGpLanes = kGpThreads / 8;   // row lanes: 8 threads x 8 columns m
 // blocks) + block) * cluster + rank: the features' largest |a| over the
 // expert's rows, then a scaled. The other CTAs: Xq to fp16, one row (of a
 // block of 64) per warp.
-static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const GwParams p) {
+template <bool WHOLE>
+__global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const GwParams p) {
   extern __shared__ int s_list[];
   __shared__ uint32_t s_max[kGpCols];
   __shared__ float s_mult[kGpCols];
@@ -367,7 +401,7 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
     const int e = eb / blocks, c0 = (eb - e * blocks) * kGpCols;
     const int lo = s_off[e], hi = s_off[e + 1];
     const int col = c0 + 8 * (tid & 7), lane_r = tid >> 3;
-    const bool in = col < p.N;   // N is a multiple of 8
+    const bool in = col < p.Np;
     const int step = p.cluster * kGpLanes;
     uint32_t top[8] = {};
     for (int r0 = lo + rank * kGpLanes + lane_r; r0 < hi; r0 += 4 * step) {
@@ -377,7 +411,7 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
       for (int u = 0; u < 4; ++u) {
         const int r = r0 + u * step;
         const bool ok = in && r < hi;
-        v[u] = ok ? __ldg(reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col)) : make_uint4(0u, 0u, 0u, 0u);
+        v[u] = ok ? gw_load8<WHOLE>(p.dy, (size_t)r, p.N, col) : make_uint4(0u, 0u, 0u, 0u);
         sc[u] = ok ? __fdiv_rn(__ldg(p.xs + r), 127.0f) : 0.f;
       }
 #pragma unroll
@@ -415,7 +449,7 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
     if (p.cluster > 1) cluster_sync_all();   // no CTA leaves while its maxima are read
     __syncthreads();
     const int pad_hi = lo + (hi - lo + 63) / 64 * 64;
-    uint16_t* dst = p.a16 + ((size_t)s_first[e] * 64) * p.N + col;
+    uint16_t* dst = p.a16 + ((size_t)s_first[e] * 64) * p.Np + col;
     float mult[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) mult[j] = s_mult[8 * (tid & 7) + j];
@@ -426,7 +460,7 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
       for (int u = 0; u < 4; ++u) {
         const int r = r0 + u * step;
         const bool ok = in && r < hi;
-        v[u] = ok ? __ldg(reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col)) : make_uint4(0u, 0u, 0u, 0u);
+        v[u] = ok ? gw_load8<WHOLE>(p.dy, (size_t)r, p.N, col) : make_uint4(0u, 0u, 0u, 0u);
         sc[u] = ok ? __fdiv_rn(__ldg(p.xs + r), 127.0f) : 0.f;
       }
 #pragma unroll
@@ -440,7 +474,7 @@ static __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const Gw
           const float a1 = __fmul_rn(__fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), sc[u]), mult[2 * j + 1]);
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(a1), "f"(a0));
         }
-        if (in && r < pad_hi) *reinterpret_cast<uint4*>(dst + (size_t)(r - lo) * p.N) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (in && r < pad_hi) *reinterpret_cast<uint4*>(dst + (size_t)(r - lo) * p.Np) = make_uint4(h[0], h[1], h[2], h[3]);
       }
     }
     griddep_launch_dependents();
@@ -686,105 +720,6 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kBxTmemCols) : "memory");
-  }
-}
-
-// ---------------------------------------------------------------------------
-// N_out not a multiple of 8 (dY's rows do not start on 16-byte boundaries):
-// tiled fp32 products on the CUDA cores, as in bwd.cuh.
-// ---------------------------------------------------------------------------
-template <int MM, int CB, bool DENSE>
-__global__ void __launch_bounds__(kBwThreads)
-bwd_dx_grp_plain_kernel(const uint16_t* __restrict__ dy, const GxParams p) {
-  extern __shared__ int s_list[];
-  __shared__ float s_a[kBwSlice][kBwTile];   // dY^T slice: [n][t]
-  __shared__ float s_b[kBwSlice][kBwTile];   // C slice: [n][k]
-  int* s_off = s_list;
-  int* s_first = s_list + p.grp.experts + 1;
-  griddep_wait();
-  if (threadIdx.x < 32) grp_build(p.grp, kBwTile, 1, 0, s_off, s_first);
-  __syncthreads();
-  if ((int)blockIdx.y >= s_first[p.grp.experts]) return;
-  const TgTile tl = tg_tile(s_off, s_first, p.grp, blockIdx.y, 1, 0, kBwTile, 1);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int k0 = blockIdx.x * kBwTile;
-  const uint8_t* codes = p.codes + (size_t)tl.e * p.N * p.cstride;
-  const uint8_t* meta = DENSE ? nullptr : p.meta + (size_t)tl.e * p.N * p.mstride;
-  float acc[4][4] = {};
-  for (int n0 = 0; n0 < p.N; n0 += kBwSlice) {
-    for (int i = tid; i < kBwSlice * kBwTile; i += kBwThreads) {
-      const int tt = i / kBwSlice, nn = i - tt * kBwSlice;
-      const int t = tl.tok0 + tt, n = n0 + nn;
-      s_a[nn][tt] = (t < tl.tok_end && n < p.N) ? bf16_to_f32(dy[(size_t)t * p.N + n]) : 0.f;
-    }
-    if (tid < kBwSlice * (kBwTile / 16)) {
-      const int nn = tid >> 2, uu = tid & 3;
-      const int n = n0 + nn, u = (k0 >> 4) + uu;
-      uint32_t cw = 0u, keep = 0u;
-      if (n < p.N) {
-        const uint8_t* cp = codes + (size_t)n * p.cstride + (size_t)u * CB;
-#pragma unroll
-        for (int b = 0; b < CB; ++b) cw |= (uint32_t)cp[b] << (8 * b);
-        keep = DENSE ? 0xFFFFu
-                     : (uint32_t)meta[(size_t)n * p.mstride + 2 * u] | ((uint32_t)meta[(size_t)n * p.mstride + 2 * u + 1] << 8);
-      }
-      int ci = 0;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float v = 0.f;
-        if ((keep >> j) & 1u) {
-          const uint32_t c2 = (cw >> (2 * ci)) & 3u;
-          v = (c2 == 1u) ? 1.f : ((c2 == 3u) ? -1.f : 0.f);
-          ++ci;
-        }
-        s_b[nn][uu * 16 + j] = v;
-      }
-    }
-    __syncthreads();
-    bw_slice_fma(s_a, s_b, ty, tx, acc);
-    __syncthreads();
-  }
-  const float g = __ldg(p.gamma + tl.e);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = tl.tok0 + ty * 4 + i;
-    if (t >= tl.tok_end) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p.dx[(size_t)t * p.K + k0 + tx * 4 + j] = f32_to_bf16_bits(__fmul_rn(g, acc[i][j]));
-  }
-}
-
-// Grid (K / 64, ceil(N_out / 64), E).
-static __global__ void __launch_bounds__(kBwThreads) bwd_dw_grp_plain_kernel(const GwParams p) {
-  extern __shared__ int s_list[];
-  __shared__ float s_a[kBwSlice][kBwTile];   // dY slice: [t][n]
-  __shared__ float s_b[kBwSlice][kBwTile];   // Xd slice: [t][k]
-  griddep_wait();
-  if (threadIdx.x < 32) grp_build(p.grp, 1, 0, 0, s_list, s_list + p.grp.experts + 1);
-  __syncthreads();
-  const int e = (int)blockIdx.z, lo = s_list[e], hi = s_list[e + 1];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int k0 = blockIdx.x * kBwTile, n0 = blockIdx.y * kBwTile;
-  float acc[4][4] = {};
-  for (int t0 = lo; t0 < hi; t0 += kBwSlice) {
-    for (int i = tid; i < kBwSlice * kBwTile; i += kBwThreads) {
-      const int tt = i / kBwTile, cc = i - tt * kBwTile;
-      const int t = t0 + tt;
-      const bool tok = t < hi;
-      s_a[tt][cc] = (tok && n0 + cc < p.N) ? bf16_to_f32(p.dy[(size_t)t * p.N + n0 + cc]) : 0.f;
-      s_b[tt][cc] = tok ? (float)p.xq[(size_t)t * p.K + k0 + cc] * __fdiv_rn(__ldg(p.xs + t), 127.0f) : 0.f;
-    }
-    __syncthreads();
-    bw_slice_fma(s_a, s_b, ty, tx, acc);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + ty * 4 + i;
-    if (n >= p.N) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      p.dw[((size_t)e * p.N + n) * p.K + k0 + tx * 4 + j] = f32_to_bf16_bits(acc[i][j]);
   }
 }
 

@@ -82,7 +82,8 @@ PROTOTYPES = {
                                                _c_p]),
     "sbn_bitlinear_grouped_x_workspace_bytes": (_c_sz, [_c_i32, _c_i32]),
     "sbn_bitlinear_grouped_grad_x": (ctypes.c_int, [_c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
-                                                    _c_p, _c_p, _c_p, _c_p, _c_p]),
+                                                    _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "sbn_bitlinear_grouped_grad_x_workspace_bytes": (_c_sz, [_c_i32, _c_i32]),
     "sbn_bitlinear_grouped_grad_w": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_p,
                                                     _c_p, _c_sz, _c_p]),
     "sbn_bitlinear_grouped_grad_w_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
@@ -753,7 +754,8 @@ def bitlinear_grouped_x(x: torch.Tensor, offsets: torch.Tensor, w: PackedExperts
 
 
 def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedExperts,
-                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
     """sbn_bitlinear_grouped_grad_x: dX of every expert's rows (bf16 [R, K])."""
     _need(dy, torch.bfloat16, "dy")
     rows, n_out = dy.shape
@@ -766,8 +768,9 @@ def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedE
     _one_device(dy, offsets, out)
     if out is None:
         out = _new((rows, w.k), torch.bfloat16, dy, stream)
+    ws = _scratch(int(lib().sbn_bitlinear_grouped_grad_x_workspace_bytes(rows, n_out)), workspace, dy, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_x", stream, _ptr(dy), rows, _ptr(offsets), w.experts, w.k, n_out,
-            w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(out))
+            w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
 
