@@ -22,8 +22,12 @@
 // fp32, 128-bit of bf16, 64-bit of codes), the persistent CTAs stride over
 // the segments of 2048 elements of all tensors. The tensor table is a kernel
 // parameter: no copy to the device, nothing to keep alive, and the call can be
-// captured into a graph. Bound by DRAM: 28 bytes per element with an fp32
-// master, its bf16 copy and fp32 states, 16 with 8-bit states.
+// captured into a graph. 28 bytes per element with an fp32 master, its bf16 copy
+// and fp32 states, 16 with 8-bit states. Measured with 8-bit states at 114
+// million elements (72 tensors): 455 us, 4.0 TB/s, 62 % of the copy rate; bound
+// by instruction issue (about 100 per element: the two roundings, the hash and
+// the blocks' maxima), no longer by DRAM. A step of 24 small tensors takes 6.6
+// us on the device.
 #pragma once
 
 #include "common.cuh"

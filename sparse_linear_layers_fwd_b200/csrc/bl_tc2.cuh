@@ -23,7 +23,7 @@
 //                 CTA and stage, four stages), for layers whose 256-token
 //                 tiles would leave CTA pairs idle: twice the tiles, each
 //                 with half the MMA work per stage.
-// A stage spans 256 positions because each stage costs the MMA thread one
+// A stage spans 256 positions because each stage costs the MMA warp one
 // mbarrier wait and one commit, time in which it issues no MMA; at 128
 // positions per stage that was as long as the stage's sparse MMAs. A K that
 // is an odd multiple of 128 ends with a half stage (the second block is
@@ -49,9 +49,14 @@
 //            output rows are not 16-byte aligned). Stores from registers
 //            competed with the MMAs and cost a quarter of the kernel's time;
 //            the tile stores cost a few percent. Then the warp arrives on
-//            its CTA's `acc_empty`. The leader's MMA thread reuses an
+//            its CTA's `acc_empty`. The leader's MMA warp reuses an
 //            accumulator once both `acc_empty` (its own CTA) and `acc_peer`
 //            have completed.
+// The TMA and MMA loops are run by whole warps, which keeps addresses and
+// descriptors in uniform registers, and one elected lane issues: 41 -> 38 us for
+// 2048 tokens through 2560 x 6912 at 6:8 with the epilogue below.
+// EPI: the epilogue is f(z + bias) + residual, z kept if asked for
+// (epi_tile.cuh); that call takes 31.5 us with its quantization.
 // All waits are bounded; a wait that gives up records SBN_ERR_TIMEOUT and
 // the CTA winds down to the closing cluster barrier.
 #pragma once

@@ -38,6 +38,15 @@
 // positions are contiguous in a row): 1 KB atoms of 8 rows x 64 columns.
 // Converting in the product's own producer warps instead, for every tile
 // again, took six times as long as its MMAs.
+// Its tiles leave through shared memory and TMA stores: from registers, each
+// lane writing its feature's 64 bytes, it took 57 us where it now takes 48.
+//
+// Where N_out is not a multiple of 8, dY's rows do not start on 16-byte
+// boundaries: dW's preparation reads them two bytes at a time, and dX gets a
+// copy of dY at a padded pitch first (bwd_pitch_kernel).
+// Measured at 8192 rows of 16 experts (K = 2048, N_out = 1408, 6:8): dX 70 us,
+// preparation 31, dW 48 (0.58 of the bf16 rate); at 1000 rows (K = 896, N_out =
+// 1000, 8:16) 18.8, 6.3 and 15.6 us.
 #pragma once
 
 #include <cuda.h>

@@ -27,7 +27,7 @@ struct LaunchDx {
     if (!set_smem_attr_once(kern, gx_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
     CUtensorMap td, tc, tm;
     const uint64_t wrows = (uint64_t)e * (uint64_t)p.N;
-    if (!encode_2d(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pitched ? pitched : dy, p.N, r, 2 * (uint64_t)round_up8(p.N),
+    if (!encode_2d(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pitched ? pitched : dy, round_up8(p.N), r, 2 * (uint64_t)round_up8(p.N),
                    kBxBK, kBxBM,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, p.cstride, wrows, p.cstride, 16 * CB, kBxBK,

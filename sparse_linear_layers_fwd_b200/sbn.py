@@ -798,6 +798,8 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
     return out
 
 
+_nbytes, _dtype_of = torch.Tensor.nbytes.__get__, torch.Tensor.dtype.__get__
+
 ADAMW_BLOCK = 256   # SBN_ADAMW_BLOCK: elements that share a scale in the 8-bit states
 
 
@@ -839,8 +841,6 @@ class AdamW:
         for p in self.params:
             _need(p, dt, "params")
         self.device = _one_device(*self.params)
-        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(1 for p in self.params if p.numel()):
-            raise ValueError("a parameter appears twice")
         if self.copies is not None:
             if dt != torch.float32:
                 raise TypeError("copies go with float32 parameters")
@@ -852,6 +852,12 @@ class AdamW:
                     raise ValueError("a copy and its parameter differ in size")
             _one_device(self.params[0], *self.copies)
         self._sizes = [p.numel() for p in self.params]
+        self._kept = self.params + (self.copies or [])
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in self._kept if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters or copies overlap, or one appears twice")
+        self._bytes = [t.nbytes for t in self._kept]
+        self._at = None   # their addresses at the last step
         # entries of sbn_adamw_tensor: eight 64-bit words each
         self._table = array.array("q", bytes(64 * len(self.params)))
         self._table[7::8] = array.array("q", self._sizes)
@@ -917,7 +923,7 @@ class AdamW:
         if gd not in (torch.float32, torch.bfloat16):
             raise TypeError(f"grads must be float32 or bfloat16, got {gd}")
         if (list(map(torch.Tensor.numel, grads)) != self._sizes or not all(map(torch.Tensor.is_contiguous, grads))
-                or any(g.dtype is not gd or g.device != self.device for g in grads)):
+                or set(map(_dtype_of, grads)) != {gd} or set(map(torch.Tensor.get_device, grads)) != {self.device.index}):
             for g in grads:
                 _need(g, gd, "grads")
             raise ValueError("a gradient differs from its parameter in size or device")
@@ -932,11 +938,18 @@ class AdamW:
         if isinstance(lr, torch.Tensor):
             lr_dev, lr = lr, 0.0
         # the parameters' own storage may have been exchanged since the last step
-        table, ptr = self._table, torch.Tensor.data_ptr
-        table[0::8] = array.array("q", map(ptr, self.params))
+        # (an address belongs to one device, so only a new one can be elsewhere)
+        table, ptr, kept = self._table, torch.Tensor.data_ptr, self._kept
+        at = array.array("q", map(ptr, kept))
+        if (list(map(_nbytes, kept)) != self._bytes or not all(map(torch.Tensor.is_contiguous, kept))
+                or at != self._at and any(t.device != self.device for t in kept)):
+            raise ValueError("a parameter or a copy changed its size, layout or device")
+        self._at = at
+        n = len(self.params)
+        table[0::8] = at[:n]
         table[1::8] = array.array("q", map(ptr, grads))
         if self.copies is not None:
-            table[6::8] = array.array("q", map(ptr, self.copies))
+            table[6::8] = at[n:]
         _run_on(self.device, "sbn_adamw", stream, table.buffer_info()[0], len(self.params),
                 int(self.params[0].dtype == torch.bfloat16), int(gd == torch.bfloat16), self.state_bits,
                 _ptr(self.step_state), float(lr), _ptr(lr_dev), float(self.betas[0]), float(self.betas[1]),

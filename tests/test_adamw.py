@@ -341,3 +341,34 @@ def test_state_dict_streams_and_refusals(sbn_lib, cuda_ok):
         sbn.AdamW([torch.zeros(8, 8, device="cuda").t()[:, :4]])
     with pytest.raises(ValueError):
         other.load_state_dict(sbn.AdamW(p).state_dict())
+
+
+@gpu
+def test_overlaps_and_exchanged_storage(sbn_lib, cuda_ok):
+    sbn = _sbn()
+    flat = torch.randn(1000, device="cuda")
+    for parts in ([flat[:600], flat[599:]], [flat, flat], [flat[:10], flat[20:30], flat[25:40]]):
+        with pytest.raises(ValueError):
+            sbn.AdamW(parts)
+    with pytest.raises(ValueError):
+        sbn.AdamW([flat], copies=[flat.view(torch.bfloat16)[:1000]])
+    opt = sbn.AdamW([flat[:600], flat[600:]], lr=0.1, weight_decay=0.0)   # neighbours are apart
+    grads = [torch.ones(600, device="cuda"), torch.ones(400, device="cuda")]
+    before = flat.clone()
+    opt.step(grads)
+    torch.cuda.synchronize()
+    assert bool((flat < before).all())
+    # storage exchanged for one of the same kind is followed, any other refused
+    p = torch.zeros(64, 8, device="cuda")
+    opt = sbn.AdamW([p], lr=0.1, weight_decay=0.0)
+    p.data = torch.ones(64, 8, device="cuda")
+    g = [torch.ones(64, 8, device="cuda")]
+    opt.step(g)
+    torch.cuda.synchronize()
+    assert bool((p < 1).all())
+    for other in (torch.ones(32, 8, device="cuda"), torch.ones(8, 64, device="cuda").t(),
+                  torch.ones(64, 8, device="cuda", dtype=torch.bfloat16), torch.ones(64, 8)):
+        p.data = other
+        with pytest.raises(ValueError):
+            opt.step(g)
+    assert int(opt.step_state[0]) == 1 and sbn.get_device_error() == 0
