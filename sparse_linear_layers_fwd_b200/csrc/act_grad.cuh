@@ -53,8 +53,19 @@ act_grad_kernel(const AgParams p) {
   griddep_wait();
   int lo = 0, hi = p.grp.rows;
   if (p.grp.offsets) {
-    lo = min(max(p.grp.offsets[e], 0), p.grp.rows);
-    hi = min(max(p.grp.offsets[e + 1], 0), p.grp.rows);
+    // as grp_build has them: the largest offset so far, so that no row belongs
+    // to two experts whatever the offsets are
+    __shared__ int s_top[kAgThreads / 32];
+    const int next = p.grp.offsets[e + 1];
+    int top = 0;
+    for (int i = tid; i <= e; i += kAgThreads) top = max(top, p.grp.offsets[i]);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) s_top[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAgThreads / 32; ++i) top = max(top, s_top[i]);
+    lo = min(top, p.grp.rows);
+    hi = min(max(next, lo), p.grp.rows);
   }
   const int step = VEC ? 1 : kAgColLanes;   // distance between a lane's columns
   const int col = c0 + (VEC ? 8 * lane_c : lane_c);

@@ -58,10 +58,17 @@ SBN_DEVFN float epi_phi(float z, float& e) {
   return z < 0.f ? q : 1.f - q;
 }
 
+// max(z, 0) that keeps a NaN.
+SBN_DEVFN float epi_relu(float z) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
+  return y;
+}
+
 SBN_DEVFN float act_f(int act, float z) {
   switch (act) {
-    case kActRelu: return fmaxf(z, 0.f);
-    case kActRelu2: { const float r = fmaxf(z, 0.f); return r * r; }
+    case kActRelu: return epi_relu(z);
+    case kActRelu2: { const float r = epi_relu(z); return r * r; }
     case kActSilu: return z * epi_sigmoid(z);
     case kActGelu: { float e; return z * epi_phi(z, e); }
     default: return z;
@@ -71,7 +78,7 @@ SBN_DEVFN float act_f(int act, float z) {
 SBN_DEVFN float act_df(int act, float z) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActRelu2: return 2.f * fmaxf(z, 0.f);
+    case kActRelu2: return 2.f * epi_relu(z);
     case kActSilu: {
       const float s = epi_sigmoid(z);
       return s * (1.f + z * (1.f - s));

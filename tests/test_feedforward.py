@@ -659,3 +659,42 @@ def test_training_step_of_an_expert_block(sbn_lib, cuda_ok):
         flips.append(int(sbn.mask_flips(up.expert(0), again.expert(0))))
     assert all(c > 0 for c in flips)
     clean(sbn)
+
+
+@gpu
+@pytest.mark.parametrize("n_out", [64, 129])
+def test_act_grad_offsets_out_of_order(sbn_lib, cuda_ok, n_out):
+    """No row belongs to two experts whatever the offsets are: dz in place is
+    formed once, and the sums are those of the clamped offsets."""
+    sbn = _sbn()
+    rows = 300
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dy = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
+    z = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
+    for bad, good in (([0, 200, 100, 150, 300], [0, 200, 200, 200, 300]), ([-7, 40, -1, 5000, 90], [0, 40, 40, 300, 300]),
+                      ([500, 0, 20, 30, 40], [300, 300, 300, 300, 300])):
+        want, wsum = sbn.act_grad(dy, z, "silu", torch.tensor(good, dtype=torch.int32, device="cuda"), out=dy.clone())
+        d = dy.clone()
+        got, gsum = sbn.act_grad(d, z, "silu", torch.tensor(bad, dtype=torch.int32, device="cuda"), out=d)
+        clean(sbn)
+        assert torch.equal(got, want) and torch.equal(gsum, wsum), bad
+
+
+@gpu
+@pytest.mark.parametrize("t", [3, 40])
+def test_nan_and_infinity_pass_through(sbn_lib, cuda_ok, t):
+    """A bias that is not finite reaches the output as in the formula: no
+    activation hides a NaN."""
+    sbn = _sbn()
+    layer = Layer(1, 64, 256, 6, 8, "nan")
+    x, q, s = acts_of(t, 256, f"nan{t}")
+    bias = torch.zeros(64, device="cuda")
+    bias[3], bias[5], bias[7] = float("nan"), float("inf"), float("-inf")
+    for act, low in (("none", float("-inf")), ("relu", 0.0), ("relu2", 0.0), ("silu", None), ("gelu", None)):
+        for y in (sbn.bitlinear_act(q, s, layer.packed.expert(0), bias=bias, act=act),
+                  sbn.bitlinear_act(q, s, layer.packed.expert(0), bias=bias, act=act, workspace=False)):
+            assert y[:, 3].isnan().all() and (y[:, 5] == float("inf")).all(), act
+            if low is not None:
+                assert (y[:, 7] == low).all(), act
+            assert y[:, [0, 1, 2, 4, 6, 8]].isfinite().all()
+    clean(sbn)
