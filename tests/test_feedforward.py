@@ -368,6 +368,10 @@ GRP_CASES = [
     ((7,) * 40, 256, 72, 8, 16),
     ((0,) * 900 + (1, 1, 40) + (0,) * 121, 128, 24, 1, 4),
     ((0,) * 1000 + (2, 1) + (0,) * 22, 128, 24, 3, 4),
+    # several tiles for each CTA: of one, three and five blocks of positions
+    ((33,) * 40, 128, 2000, 6, 8),
+    ((40,) * 30, 384, 1500, 2, 4),
+    ((700, 0, 450, 900), 640, 2100, 8, 8),
 ]
 
 
