@@ -55,7 +55,6 @@
 #include "bl_gemv.cuh"
 #include "bl_tc.cuh"
 #include "bl_tc_grp.cuh"
-#include "bwd.cuh"
 #include "bwd_tc.cuh"
 #include "common.cuh"
 #include "grp.cuh"
