@@ -11,8 +11,8 @@
 // cluster start and end together, and with eight of them per block of columns a
 // batch over 16 experts ran at a third of the bandwidth. Where N_out is not a
 // multiple of 8 a lane takes every 8th column with 2-byte accesses.
-// Measured at 4096 rows of 6912 features: 31.6 us, 5.4 TB/s, 84 % of the copy
-// rate; at 509 rows the kernel takes 9 us, the call 13.4.
+// Measured at 4096 rows of 6912 features, 16 experts: 32 us, 5.3 TB/s, 82 % of
+// the copy rate; at 509 rows the kernel takes 9 us, the call 13.8.
 #pragma once
 
 #include "common.cuh"
@@ -54,16 +54,12 @@ act_grad_kernel(const AgParams p) {
   int lo = 0, hi = p.grp.rows;
   if (p.grp.offsets) {
     // as grp_build has them: the largest offset so far, so that no row belongs
-    // to two experts whatever the offsets are
-    __shared__ int s_top[kAgThreads / 32];
+    // to two experts whatever the offsets are (every warp for itself: with a
+    // barrier 4096 rows of 16 experts took 36 us, not 32)
     const int next = p.grp.offsets[e + 1];
     int top = 0;
-    for (int i = tid; i <= e; i += kAgThreads) top = max(top, p.grp.offsets[i]);
+    for (int i = tid & 31; i <= e; i += 32) top = max(top, p.grp.offsets[i]);
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) s_top[tid >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAgThreads / 32; ++i) top = max(top, s_top[i]);
     lo = min(top, p.grp.rows);
     hi = min(max(next, lo), p.grp.rows);
   }
