@@ -32,6 +32,15 @@ namespace sbn {
 
 constexpr int kGgMaxRows = 16;
 constexpr int kGgMaxSlots = 16;
+// Arrival barriers, taken in turn by the tiles of a CTA (tile % kGgArrivals,
+// whatever its slot). A wait by parity for tile t must not meet a barrier whose
+// earlier tile t - kGgArrivals is still to come. A warp's tiles lie at most 31
+// apart (items are dealt out to 31 warps), and a tile that has landed was
+// issued, so every tile a ring before it had been consumed: with at least 31 +
+// slots barriers, t - kGgArrivals is one of those. One barrier per slot let
+// warps that start two rounds ahead (K <= 256) pass before any copy had landed.
+constexpr int kGgArrivals = 48;
+static_assert(kGgArrivals >= kGvConsumerWarps + kGgMaxSlots, "no wait by parity may be two phases off");
 
 struct GgLayout {
   uint32_t sel, list, rmax, scale, mult, full, empty, cnt, acc, x, codes, meta, total;
@@ -52,7 +61,7 @@ __host__ __device__ inline GgLayout gg_layout(int tiles, int nt, int t, int k, i
     L.scale = L.rmax + kGgMaxRows * 4;
     L.mult = L.scale + kGgMaxRows * 4;
     L.full = gv_align128(L.mult + kGgMaxRows * 4);
-    L.empty = L.full + 8 * S;
+    L.empty = L.full + 8 * kGgArrivals;
     L.cnt = L.empty + 8 * S;
     L.acc = gv_align128(L.cnt + 4 * S);          // [S][16][nt] int32
     L.x = gv_align128(L.acc + (size_t)S * 16 * nt * 4);
@@ -124,8 +133,8 @@ bl_gemv_grp_kernel(const GgParams p) {
   if (warp == kGvConsumerWarps) {
     // ---- producer warp ----
     if (lane < kGgMaxRows) s_rmax[lane] = 0u;
+    for (int i = lane; i < kGgArrivals; i += 32) mbar_init(&s_full[i], 1);
     if (lane < S) {
-      mbar_init(&s_full[lane], 1);
       mbar_init(&s_empty[lane], 1);
       s_cnt[lane] = 0;
     }
@@ -178,9 +187,10 @@ bl_gemv_grp_kernel(const GgParams p) {
         const uint32_t rows = (uint32_t)min(16, p.N - r);
         const uint32_t cbytes = rows * (uint32_t)p.cstride;
         const uint32_t mbytes = DENSE ? 0u : rows * (uint32_t)p.mstride;
-        mbar_arrive_expect_tx(&s_full[slot], cbytes + mbytes);
-        bulk_g2s(s_codes + (size_t)slot * 16 * p.cstride, p.codes + row * p.cstride, cbytes, &s_full[slot]);
-        if (!DENSE) bulk_g2s(s_meta + (size_t)slot * 16 * p.mstride, p.meta + row * p.mstride, mbytes, &s_full[slot]);
+        uint64_t* full = &s_full[i % kGgArrivals];
+        mbar_arrive_expect_tx(full, cbytes + mbytes);
+        bulk_g2s(s_codes + (size_t)slot * 16 * p.cstride, p.codes + row * p.cstride, cbytes, full);
+        if (!DENSE) bulk_g2s(s_meta + (size_t)slot * 16 * p.mstride, p.meta + row * p.mstride, mbytes, full);
       }
     }
     return;   // every copy is waited for by the consumers before they leave
@@ -274,7 +284,7 @@ bl_gemv_grp_kernel(const GgParams p) {
     const int r0 = ((begin + tile) - a * tpe) * 16;   // first weight row of the tile
     const int4 ex = s_list[a];
     const int row0 = ex.x, nrow = ex.y;
-    if (!mbar_wait(&s_full[slot], (tile / S) & 1u)) break;
+    if (!mbar_wait(&s_full[tile % kGgArrivals], (tile / kGgArrivals) & 1u)) break;
     const int span = kit * 256 + 64 * t;   // first position of this thread's 64
     const bool valid = span < p.K;
     uint32_t cw[2][CB];

@@ -1,0 +1,110 @@
+"""The feed-forward calls where they can go wrong beside the sizes of
+test_feedforward.py, whose references and tolerances serve here too."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_feedforward import acts_of, clean, close, epilogue_inputs, reference
+
+gpu = pytest.mark.gpu
+
+SMEM = 227 * 1024    # shared memory of a CTA
+
+
+def _sbn():
+    from sparse_linear_layers_fwd_b200 import sbn
+    return sbn
+
+
+class Packed:
+    """Experts quantized on the device, their ternary matrices read back from
+    the packed arrays (the quantizer's own parity tests pin those)."""
+
+    def __init__(self, experts, n_out, k, n, m, tag):
+        sbn = _sbn()
+        g = torch.Generator(device="cuda").manual_seed(len(tag) + n_out + k)
+        w = (0.02 * torch.randn(experts, n_out, k, device="cuda", generator=g)).to(torch.bfloat16)
+        self.packed = p = sbn.quantize_experts(w, n, m)
+        kept = n_out * (k * n // m)
+        two = torch.tensor([0, 2, 4, 6], device="cuda")
+        bit = torch.arange(8, device="cuda")
+        value = torch.tensor([0, 1, 0, -1], dtype=torch.int8, device="cuda")
+        self.dense = []
+        for e in range(experts):
+            codes = value[((p.codes[e][..., None] >> two) & 3).long()].view(n_out, -1)[:, :k * n // m]
+            if n == m:
+                self.dense.append(codes.double())
+                continue
+            keep = ((p.meta[e][..., None] >> bit) & 1).bool().view(n_out, -1)[:, :k]
+            assert int(keep.sum()) == kept
+            d = torch.zeros(n_out, k, dtype=torch.float64, device="cuda")
+            d[keep] = codes.reshape(-1).double()
+            self.dense.append(d)
+        self.gamma = p.gamma.double()
+
+        class Dense(list):
+            shape = (experts, n_out, k)
+        self.dense = Dense(self.dense)
+
+
+# rows per expert, K, N_out, pattern: one to three items of 256 positions to a
+# tile and 17 to 56 tiles to a CTA, 8 and 16 rows, one layer and experts; and rows
+# so long that shared memory leaves a CTA fewer slots than it has tiles
+RING_CASES = [
+    ((1,) * 16, 128, 8000, 6, 8),
+    ((1,) * 16, 256, 8192, 2, 4),
+    ((1,) * 8, 256, 5057, 6, 8),
+    ((1,) * 8, 512, 8000, 8, 8),
+    ((2, 0, 1, 1) * 4, 512, 5000, 8, 16),
+    ((1,) * 12, 768, 4000, 4, 8),
+    ((1,), 256, 50304, 6, 8),
+    ((7,), 128, 60001, 1, 4),
+    ((1,), 8192, 19000, 6, 8),
+    ((2, 2), 4096, 19000, 12, 16),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", RING_CASES, ids=[f"e{len(c[0])}_r{sum(c[0])}_k{c[1]}_n{c[2]}_{c[3]}of{c[4]}" for c in RING_CASES])
+def test_decode_ring_reused(sbn_lib, cuda_ok, case):
+    """At most 16 rows whose CTAs walk more 16-feature tiles than their ring of
+    shared memory has slots: every slot is waited for, filled and handed back
+    several times. INT8 and bf16 activations, the same bits on every run."""
+    sbn = _sbn()
+    sizes, k, n_out, n, m = case
+    rows, experts = sum(sizes), len(sizes)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    active = sum(1 for s in sizes if s)
+    least = active * ((n_out + 15) // 16) // sms
+    slots = min(16, SMEM // (16 * (sbn.codes_row_bytes(k, n, m) + sbn.meta_row_bytes(k, n, m))))
+    assert least > slots, "every CTA must have more tiles than slots"
+    layer = Packed(experts, n_out, k, n, m, "ring")
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    spans = list(zip(off[:-1].tolist(), off[1:].tolist()))
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    x, q, s = acts_of(rows, k, f"ring{case}"[:40])
+    bias, res = epilogue_inputs(rows, n_out, experts)
+    y, ytol, z, ztol = reference(layer, q, s, spans, bias, "silu", res)
+    tiny = torch.empty(16, dtype=torch.uint8, device="cuda")   # too small for any other route
+    first = None
+    for turn in range(6):
+        out = torch.full((rows, n_out), 77.0, dtype=torch.bfloat16, device="cuda")
+        oz = torch.full_like(out, 78.0)
+        if turn % 2:
+            sbn.bitlinear_grouped(q, s, o, layer.packed, bias=bias, act="silu", residual=res, out=out, out_z=oz)
+        else:
+            sbn.bitlinear_grouped_x(x, o, layer.packed, bias=bias, act="silu", residual=res, out=out, out_z=oz,
+                                    workspace=tiny)
+        clean(sbn)
+        close(out, y, ytol, f"y {turn}")
+        close(oz, z, ztol, f"z {turn}")
+        if first is None:
+            first = (out, oz)
+        assert torch.equal(out, first[0]) and torch.equal(oz, first[1])
+    if experts == 1:
+        w = layer.packed.expert(0)
+        for out in (sbn.bitlinear_x_act(x, w, bias=bias[0], act="silu", residual=res, workspace=tiny),
+                    sbn.bitlinear_act(q, s, w, bias=bias[0], act="silu", residual=res)):
+            assert torch.equal(out, first[0])
+    clean(sbn)
