@@ -66,14 +66,16 @@ act_grad_kernel(const AgParams p) {
   const int step = VEC ? 1 : kAgColLanes;   // distance between a lane's columns
   const int col = c0 + (VEC ? 8 * lane_c : lane_c);
   float sum[8] = {};
-  for (int r0 = lo + rank * kAgLanes + lane_r; r0 < hi; r0 += kAgUnroll * cs * kAgLanes) {
+  // unsigned: up to kAgUnroll * cs * kAgLanes past the last row, which may be the 2^31st
+  const unsigned end = (unsigned)hi, stride = (unsigned)(cs * kAgLanes);
+  for (unsigned r0 = (unsigned)lo + (unsigned)(rank * kAgLanes + lane_r); r0 < end; r0 += kAgUnroll * stride) {
     uint4 dv[kAgUnroll], zv[kAgUnroll];
     float d[8], z[8];
     if (VEC) {
 #pragma unroll
       for (int u = 0; u < kAgUnroll; ++u) {
-        const int r = r0 + u * cs * kAgLanes;
-        if (r < hi && col < p.N) {
+        const unsigned r = r0 + u * stride;
+        if (r < end && col < p.N) {
           dv[u] = *reinterpret_cast<const uint4*>(p.dy + (size_t)r * p.N + col);
           zv[u] = *reinterpret_cast<const uint4*>(p.z + (size_t)r * p.N + col);
         }
@@ -81,8 +83,8 @@ act_grad_kernel(const AgParams p) {
     }
 #pragma unroll
     for (int u = 0; u < kAgUnroll; ++u) {
-      const int r = r0 + u * cs * kAgLanes;
-      if (r >= hi || col >= p.N) continue;
+      const unsigned r = r0 + u * stride;
+      if (r >= end || col >= p.N) continue;
       const size_t at = (size_t)r * p.N + col;
       if (VEC) {
         const uint32_t dw[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w}, zw[4] = {zv[u].x, zv[u].y, zv[u].z, zv[u].w};

@@ -108,3 +108,26 @@ def test_decode_ring_reused(sbn_lib, cuda_ok, case):
                     sbn.bitlinear_act(q, s, w, bias=bias[0], act="silu", residual=res)):
             assert torch.equal(out, first[0])
     clean(sbn)
+
+
+@gpu
+@pytest.mark.parametrize("rows", [2 ** 31 - 1, 2 ** 31 - 700])
+def test_act_grad_at_the_last_rows(sbn_lib, cuda_ok, rows):
+    """One feature and as many rows as a call may have: the rows behind the
+    last are counted, not wrapped around. Only the last 3000 belong to a group,
+    the very last to one of its own; dz and the sums are small whole numbers."""
+    sbn = _sbn()
+    n = 3000
+    dy = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda")
+    z = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda")
+    dy[:2 * n] = 5.0
+    dy[-2 * n:] = 5.0
+    v = torch.arange(n, device="cuda") % 7 - 3
+    dy[-n:, 0] = v.to(torch.bfloat16)
+    z[-n:] = 1.0
+    o = torch.tensor([rows - n, rows - 1, rows], dtype=torch.int32, device="cuda")
+    _, db = sbn.act_grad(dy, z, "relu2", offsets=o, out=dy)
+    clean(sbn)
+    assert torch.equal(dy[-n:, 0], (2 * v).to(torch.bfloat16))
+    assert bool((dy[-2 * n:-n] == 5.0).all()) and bool((dy[:2 * n] == 5.0).all())
+    assert db.view(-1).tolist() == [float(2 * v[:-1].sum()), float(2 * v[-1])]
