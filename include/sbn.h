@@ -629,7 +629,8 @@ sbn_status sbn_probe_i8_sparse_mma(int32_t iters, int32_t* pairs, void* stream);
  * Test hook of the failure detection (no counterpart in the method): runs one
  * of the library's bounded device waits on a condition that never comes, with
  * a limit of limit_ns (1e3..1e8) nanoseconds, on `stream`. which = 0: an
- * mbarrier wait (the kind every pipelined kernel uses); which = 1: the grid
+ * mbarrier wait (the kind every pipelined kernel uses), by one thread and by
+ * a whole warp of which half waits in vain; which = 1: the grid
  * barrier of the weight quantizer. The wait gives up, records the timeout in
  * the device error word and the kernel returns normally, so the next
  * sbn_get_device_error returns SBN_ERR_TIMEOUT (and clears the word). No

@@ -47,6 +47,32 @@ SBN_DEVFN bool mbar_wait(uint64_t* bar, uint32_t parity, unsigned long long limi
   return false;
 }
 
+// The waits of a whole warp (every lane calls, none waits for another): all
+// lanes get the same answer, by a vote. Lanes that disagreed about a wait that
+// ran out would part, and those that go on meet the next warp-wide step alone.
+// All but the first try is out of line: inlined into every loop of a kernel
+// whose warps take many roles, it cost the grouped forward 4 % (40.4 us, not
+// 39.1, at 256 rows of 64 experts; without the vote 38).
+static __device__ __noinline__ bool mbar_wait_rest(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  return mbar_wait(bar, parity, limit_ns);
+}
+SBN_DEVFN bool mbar_wait_lane(uint64_t* bar, uint32_t parity, unsigned long long limit_ns = kMbarWaitNs) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kMbarSuspendNs)
+      : "memory");
+  return done != 0u || mbar_wait_rest(bar, parity, limit_ns);
+}
+SBN_DEVFN bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned long long limit_ns = kMbarWaitNs) {
+  return __all_sync(0xffffffffu, mbar_wait_lane(bar, parity, limit_ns));
+}
+// Two barriers, one vote.
+SBN_DEVFN bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) {
+  return __all_sync(0xffffffffu, mbar_wait_lane(bar, parity) && mbar_wait_lane(bar2, parity2));
+}
+
 // One non-blocking probe of the phase of the given parity (no suspension,
 // no time bound): true if it has completed. Callers fall back to mbar_wait.
 SBN_DEVFN bool mbar_test(uint64_t* bar, uint32_t parity) {

@@ -284,7 +284,7 @@ bl_gemv_grp_kernel(const GgParams p) {
     const int r0 = ((begin + tile) - a * tpe) * 16;   // first weight row of the tile
     const int4 ex = s_list[a];
     const int row0 = ex.x, nrow = ex.y;
-    if (!mbar_wait(&s_full[tile % kGgArrivals], (tile / kGgArrivals) & 1u)) break;
+    if (!mbar_wait_warp(&s_full[tile % kGgArrivals], (tile / kGgArrivals) & 1u)) break;
     const int span = kit * 256 + 64 * t;   // first position of this thread's 64
     const bool valid = span < p.K;
     uint32_t cw[2][CB];

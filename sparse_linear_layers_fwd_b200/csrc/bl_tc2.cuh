@@ -223,7 +223,7 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
       const int tok0 = (tile / row_pairs) * C::BN + (int)rank * C::HALF;
       const int row0 = (tile % row_pairs) * 256 + (int)rank * 128;
       for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&empty[s], ph)) { ok = false; break; }
         const uint32_t fb = full0 + 8u * (uint32_t)s;
         uint8_t* st = smem + (size_t)s * C::STAGE;
         if (lead) {
@@ -264,10 +264,10 @@ bl_tc2_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant_
       for (int tile = pair; tile < n_tiles && ok; tile += npairs, ++jt) {
         const int b = jt & 1;
         const uint32_t pa = ((jt >> 1) & 1u) ^ 1u;
-        if (!mbar_wait(&acc_empty[b], pa) || !mbar_wait(&acc_peer[b], pa)) break;
+        if (!mbar_wait_warp(&acc_empty[b], pa, &acc_peer[b], pa)) break;
         const uint32_t d_tmem = tmem + (uint32_t)(b * C::BN);
         for (int ks = 0; ks < nst; ++ks) {
-          if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+          if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
           tc_fence_after();
           const uint32_t e_tmem = tmem + C::ECOL + 8u * (uint32_t)s;
           const uint64_t so = (uint64_t)(s * (C::STAGE / 16));

@@ -300,7 +300,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       if (!t.nmma) continue;
       const int nmma = __shfl_sync(0xffffffffu, t.nmma, 0), tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait(&b_empty[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&b_empty[s], ph)) { ok = false; break; }
         uint8_t* dst = smem + (size_t)s * kTgBlockBytes;
         if (lead) {
           mbar_arrive_expect_tx(&b_full[s], (uint32_t)nmma * 128u);
@@ -327,7 +327,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       // rows past the expert's are expanded, never stored
       const int row = __shfl_sync(0xffffffffu, t.e * p.N + t.row0, 0);
       for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&p_empty[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&p_empty[s], ph)) { ok = false; break; }
         uint8_t* dst = packed + s * kTgPackedBytes;
         if (lead) {
           mbar_arrive_expect_tx(&p_full[f], (uint32_t)(kTgBM * kTgSpan * (8 * CB + (DENSE ? 0 : 16))));
@@ -357,10 +357,10 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       if (!nmma) continue;
       const uint32_t idesc = __shfl_sync(0xffffffffu, kTgIdesc0 | ((uint32_t)(nmma >> 3) << 17), 0);
       const int b = used & 1;
-      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      if (!mbar_wait_warp(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
       const uint32_t d_tmem = tmem + (uint32_t)(b * kTgBN);
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait(&b_full[s], ph) || !mbar_wait(&a_full[a], pa)) { ok = false; break; }
+        if (!mbar_wait_warp(&b_full[s], ph, &a_full[a], pa)) { ok = false; break; }
         tc_fence_after();
         const uint64_t bdesc = bdesc0 + (uint64_t)(s * (kTgBlockBytes / 16));
         const uint32_t a_tmem = tmem + kTgACol + 32u * (uint32_t)a;
@@ -408,7 +408,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         // before the slot's previous stage has landed, but never before the one
         // before that (it has seen the MMA of the block 2 kTgSlots back).
         const int st = it + kb / kTgSpan, ps = st % kTgPacked, j = kb % kTgSpan;
-        if (!mbar_wait(&p_full[st % (2 * kTgPacked)], (uint32_t)(st / (2 * kTgPacked)) & 1u)) { ok = false; break; }
+        if (!mbar_wait_warp(&p_full[st % (2 * kTgPacked)], (uint32_t)(st / (2 * kTgPacked)) & 1u)) { ok = false; break; }
         const uint2* cp = reinterpret_cast<const uint2*>(packed + ps * kTgPackedBytes + (i * kTgSpan + j) * 8 * CB);
         uint32_t cw[2][CB];
 #pragma unroll
@@ -424,7 +424,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
         uint32_t w[16], v[16];
         tg_expand64<MM, CB, DENSE>(cw[0], m0, sel, w);
         tg_expand64<MM, CB, DENSE>(cw[1], m1, sel, v);
-        if (!mbar_wait(&a_empty[g], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&a_empty[g], ph)) { ok = false; break; }
         tc_fence_after();
         tmem_st16(a_tmem, w);
         tmem_st16(a_tmem + 16u, v);
@@ -463,7 +463,7 @@ bl_tc_grp_kernel(const __grid_constant__ CUtensorMap tmap_x64, const __grid_cons
       uint4 res[4];
       epi_load_residual(p.ep, out, row_w, tok_w, t.tok_end, lane, res);
       float xs_n = tok_w + lane < t.tok_end ? __ldg(p.xs + tok_w + lane) : 0.f;
-      if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
+      if (!mbar_wait_warp(&acc_full[b], (used >> 1) & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1

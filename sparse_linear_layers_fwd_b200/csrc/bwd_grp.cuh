@@ -165,7 +165,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       if (!t.nmma) continue;
       const int tok0 = __shfl_sync(0xffffffffu, t.tok0, 0);
       for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&empty[s], ph)) { ok = false; break; }
         uint8_t* st = smem + (size_t)s * kBxStageBytes;
         if (lead) {
           mbar_arrive_expect_tx(&full[s], kBxABytes);
@@ -189,7 +189,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       const int row = __shfl_sync(0xffffffffu, t.e * p.N, 0), k0 = __shfl_sync(0xffffffffu, t.row0, 0);
       for (int ks = 0; ks < nst; ++ks, ++it) {
         const int s = it % kGxPacked;
-        if (!mbar_wait(&p_empty[s], ((it / kGxPacked) & 1u) ^ 1u)) { ok = false; break; }
+        if (!mbar_wait_warp(&p_empty[s], ((it / kGxPacked) & 1u) ^ 1u)) { ok = false; break; }
         uint8_t* dst = packed + s * kGxPackedBytes;
         if (lead) {
           mbar_arrive_expect_tx(&p_full[s], (uint32_t)(kBxBK * (16 * CB + (DENSE ? 0 : 32))));
@@ -211,10 +211,10 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       const TgTile t = tile_at(k);
       if (!t.nmma) continue;
       const int b = used & 1;
-      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      if (!mbar_wait_warp(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
       const uint32_t d_tmem = tmem + (uint32_t)(b * kBxBN);
       for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
         tc_fence_after();
         const uint64_t so = (uint64_t)(s * (kBxStageBytes / 16));
         if (lead) {
@@ -254,7 +254,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       it = end;
       for (; mine < end; mine += 2) {
         const int ps = mine % kGxPacked;
-        if (!mbar_wait(&p_full[ps], (mine / kGxPacked) & 1u)) { ok = false; break; }
+        if (!mbar_wait_warp(&p_full[ps], (mine / kGxPacked) & 1u)) { ok = false; break; }
         const uint32_t* cp = reinterpret_cast<const uint32_t*>(packed + ps * kGxPackedBytes + ol * 16 * CB + q * 4 * CB);
         const uint2* mp = reinterpret_cast<const uint2*>(packed + ps * kGxPackedBytes + kBxBK * 16 * CB + ol * 32 + q * 8);
         uint32_t cw[CB], mw[2] = {0u, 0u};
@@ -266,7 +266,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
           mw[1] = m.y;
         }
         const int s = mine % kBxStages;
-        if (!mbar_wait(&empty[s], ((mine / kBxStages) & 1u) ^ 1u)) { ok = false; break; }
+        if (!mbar_wait_warp(&empty[s], ((mine / kBxStages) & 1u) ^ 1u)) { ok = false; break; }
         uint8_t* row = row0 + (size_t)s * kBxStageBytes;
         *reinterpret_cast<uint4*>(row + ((0 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 0>(cw, mw, sel);
         *reinterpret_cast<uint4*>(row + ((1 ^ r) << 4)) = gx_expand8<MM, CB, DENSE, 1>(cw, mw, sel);
@@ -295,7 +295,7 @@ bwd_dx_grp_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_cons
       const int b = used & 1;
       const int row = t.tok0 + 32 * q + lane;
       const float gm = __ldg(p.gamma + t.e);
-      if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
+      if (!mbar_wait_warp(&acc_full[b], (used >> 1) & 1u)) break;
       ++used;
       tc_fence_after();
 #pragma unroll 1
@@ -605,7 +605,7 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       const int b0 = s_first[e], nst = s_first[e + 1] - b0;
       const int o0 = (local / col_tiles) * kGwBM, k0 = (local % col_tiles) * kGwBN;
       for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&empty[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&empty[s], ph)) { ok = false; break; }
         uint8_t* st = smem + (size_t)s * kGwStageBytes;
         const int row = __shfl_sync(0xffffffffu, (b0 + ks) * kGwBK, 0);
         if (lead) {
@@ -636,10 +636,10 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       const int nst = s_first[e + 1] - s_first[e];
       if (nst == 0) continue;
       const int b = used & 1;
-      if (!mbar_wait(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
+      if (!mbar_wait_warp(&acc_empty[b], ((used >> 1) & 1u) ^ 1u)) break;
       const uint32_t d_tmem = tmem + (uint32_t)(b * kGwBN);
       for (int ks = 0; ks < nst; ++ks) {
-        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+        if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
         tc_fence_after();
         const uint64_t so = (uint64_t)(s * (kGwStageBytes / 16));
         if (lead) {
@@ -674,7 +674,7 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       const int o = (local / col_tiles) * kGwBM + 32 * q + lane, k0 = (local % col_tiles) * kGwBN;
       const float sc = any && o < p.N ? __ldg(p.scale + (size_t)e * p.N + o) : 0.f;
       if (any) {
-        if (!mbar_wait(&acc_full[b], (used >> 1) & 1u)) break;
+        if (!mbar_wait_warp(&acc_full[b], (used >> 1) & 1u)) break;
         ++used;
         tc_fence_after();
       }

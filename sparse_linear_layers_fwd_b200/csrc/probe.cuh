@@ -128,18 +128,26 @@ __global__ void __launch_bounds__(kPkThreads, 1) i8_sparse_peak_kernel(int iters
 
 __device__ uint32_t g_selftest_counter;
 
-// which 0: an mbarrier (one expected arrival) that nobody arrives on; which
+// which 0: an mbarrier (one expected arrival) that nobody arrives on, waited
+// for by one thread, then by half of a warp while the other half waits for one
+// that has completed: a lane that is told all went well clears the error. which
 // 1: the grid barrier of the weight quantizer with a target no launch reaches.
 __global__ void wait_selftest_kernel(int which, unsigned long long limit_ns) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, done;
   __shared__ int s_abort;
   if (which == 0) {
     if (threadIdx.x == 0) {
       mbar_init(&bar, 1);
+      mbar_init(&done, 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncthreads();
-    if (threadIdx.x == 0) mbar_wait(&bar, 0u, limit_ns);
+    if (threadIdx.x == 0) {
+      mbar_arrive(&done);
+      mbar_wait(&bar, 0u, limit_ns);
+    }
+    __syncthreads();
+    if (mbar_wait_warp(threadIdx.x < 16 ? &bar : &done, 0u, limit_ns)) atomicExch(&g_dev_error, kDevErrNone);
   } else {
     if (threadIdx.x == 0) g_selftest_counter = 0u;   // one CTA: this launch's own counter
     __threadfence();

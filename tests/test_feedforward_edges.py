@@ -131,3 +131,17 @@ def test_act_grad_at_the_last_rows(sbn_lib, cuda_ok, rows):
     assert torch.equal(dy[-n:, 0], (2 * v).to(torch.bfloat16))
     assert bool((dy[-2 * n:-n] == 5.0).all()) and bool((dy[:2 * n] == 5.0).all())
     assert db.view(-1).tolist() == [float(2 * v[:-1].sum()), float(2 * v[-1])]
+
+
+@gpu
+@pytest.mark.parametrize("limit_ns", [1000, 200_000])
+def test_a_warp_gives_up_as_one(sbn_lib, cuda_ok, limit_ns):
+    """Half a warp waits for a barrier that never comes, half for one that has:
+    no lane may be told that the wait went well (it would clear the error)."""
+    sbn = _sbn()
+    clean(sbn)
+    for _ in range(20):
+        sbn.selftest_wait_timeout(0, limit_ns)
+        torch.cuda.synchronize()
+        assert sbn.SBN_STATUS[sbn.get_device_error()] == "SBN_ERR_TIMEOUT"
+    clean(sbn)
