@@ -356,6 +356,7 @@ bl_gemv_grp_kernel(const GgParams p) {
       __threadfence_block();
     }
     if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+    __syncwarp();   // the other warps' sums, which lane 0 has seen counted, before every lane's reads
     // ---- epilogue of the tile: 16 outputs of every row of the expert ----
     const float gm = __int_as_float(ex.w);
     for (int i = lane; i < 16 * nrow; i += 32) {
