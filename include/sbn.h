@@ -565,8 +565,9 @@ size_t sbn_bitlinear_grouped_grad_w_workspace_bytes(int32_t rows, int32_t expert
  *                 v = (code * scale)^2. Codes round up with the probability that
  *                 keeps the expectation of m and of v, from a hash of (seed, t,
  *                 index of the tensor in the call, index of the element); a
- *                 positive r never becomes 0. All-zero codes with any finite
- *                 scales are the state before the first step.
+ *                 positive r never becomes 0. An m or r that is not finite becomes the
+ *                 NaN code and leaves its block's scale alone. All-zero codes with
+ *                 any finite scales are the state before the first step.
  *     copy_bf16   optional (p_bf16 = 0): bf16 copy of the updated p, the
  *                 input of sbn_quantize_weights.
  *     numel       elements, 0 <= numel < 2^31. No two entries may overlap.

@@ -16,7 +16,9 @@
 // gives the random bits): with rounding to nearest, v would never move, since
 // one step changes it by at most 1 - b2 of itself, less than half a code. r
 // rather than v is held because its range is half as many binades; a
-// positive r never becomes code 0, so a denominator cannot vanish.
+// positive r never becomes code 0, so a denominator cannot vanish. What is not
+// finite becomes the NaN code (e4m3 has no infinity) and does not count for the
+// block's scale, so its neighbours keep their codes.
 //
 // One warp owns a block of 256 elements, eight to a lane (256-bit accesses of
 // fp32, 128-bit of bf16, 64-bit of codes), the persistent CTAs stride over
@@ -204,6 +206,13 @@ SBN_DEVFN void aw_load_codes(const uint8_t* p, size_t i, int have, bool vec, flo
   for (int j = 0; j < 8; ++j) r[j] = __fmul_rn(r[j], scale);
 }
 
+// max(a, |b|) that keeps a NaN.
+SBN_DEVFN float aw_max_abs(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+  return y;
+}
+
 // Codes of eight elements of a warp's block and the block's scale (lane 0).
 // ROOT: r = sqrt(v), with the high half of the random words; else m, the low.
 template <bool ROOT>
@@ -211,14 +220,29 @@ SBN_DEVFN void aw_store_codes(uint8_t* p, float* scale, size_t i, int have, bool
                               const uint32_t (&h)[8]) {
   float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(r[j]));
-  const int e = aw_scale_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  for (int j = 0; j < 8; ++j) top = aw_max_abs(top, r[j]);
+  uint32_t top_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top)), lost = 0u;
+  if (top_bits >= 0x7F800000u) {   // the same for every lane: an infinity or a NaN somewhere in the block
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (isfinite(r[j])) top = fmaxf(top, fabsf(r[j]));
+      else lost |= 1u << j;
+    }
+    top_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  }
+  const int e = aw_scale_exp(top_bits);
   const float up = aw_pow2(7 - e);
   float q[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float y = __fmul_rn(fabsf(r[j]), up);
     q[j] = ROOT ? aw_round_root(y, h[j] >> 16) : copysignf(aw_round(y, h[j] & 0xFFFFu), r[j]);
+  }
+  if (lost) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (lost >> j & 1u) q[j] = __uint_as_float(0x7FC00000u);
   }
   uint2 c;
   c.x = (uint32_t)aw_encode2(q[0], q[1]) | ((uint32_t)aw_encode2(q[2], q[3]) << 16);

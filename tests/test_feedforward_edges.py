@@ -145,3 +145,37 @@ def test_a_warp_gives_up_as_one(sbn_lib, cuda_ok, limit_ns):
         torch.cuda.synchronize()
         assert sbn.SBN_STATUS[sbn.get_device_error()] == "SBN_ERR_TIMEOUT"
     clean(sbn)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_keeps_what_is_not_finite(sbn_lib, cuda_ok, bits):
+    """NaN and infinite gradients: p, m and v of these elements are not finite
+    afterwards (8 bits: the NaN code) and stay so; all others and the scales are
+    those of a run in which they were zero, bit for bit."""
+    sbn = _sbn()
+    n = 1000
+    g = torch.Generator(device="cuda").manual_seed(6)
+    p0 = 0.02 * torch.randn(n, device="cuda", generator=g)
+    g0 = 1e-3 * torch.randn(n, device="cuda", generator=g)
+    bad = {0: float("nan"), 7: float("inf"), 200: float("-inf"), 255: float("nan"), 300: float("inf"), 999: float("nan")}
+    at = torch.tensor(sorted(bad), device="cuda")
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    g0[at] = 0.0
+    runs = []
+    for broken in (False, True):
+        p, grad = p0.clone(), g0.clone()
+        if broken:
+            grad[at] = torch.tensor([bad[i] for i in sorted(bad)], device="cuda")
+        opt = sbn.AdamW([p], state_bits=bits, seed=3)
+        opt.step([grad])
+        opt.step([g0])
+        clean(sbn)
+        runs.append([p, opt.m[0].float(), opt.v[0].float()] + ([opt.m_scales[0], opt.v_scales[0]] if bits == 8 else []))
+    for a, b in zip(*(r[:3] for r in runs)):
+        assert torch.equal(a[rest], b[rest])
+        assert not b[at].isfinite().any()
+    assert all(torch.equal(a, b) for a, b in zip(*(r[3:] for r in runs)))
+    if bits == 8:
+        assert runs[1][1][at].isnan().all() and runs[1][2][at].isnan().all()
