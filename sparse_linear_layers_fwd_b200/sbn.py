@@ -889,6 +889,16 @@ class AdamW:
             raise ValueError("scales go with 8-bit states")
         return [-(-n // ADAMW_BLOCK) for n in self._sizes]
 
+    step_state = property(lambda self: self._step_state)
+
+    @step_state.setter
+    def step_state(self, t):
+        _need(t, torch.int32, "step_state")
+        if t.numel() != 2:
+            raise ValueError("step_state must have two elements")
+        _one_device(self.params[0], t)
+        self._step_state = t
+
     m = property(lambda self: self._m)
     v = property(lambda self: self._v)
     m_scales = property(lambda self: self._ms)

@@ -179,3 +179,19 @@ def test_adamw_keeps_what_is_not_finite(sbn_lib, cuda_ok, bits):
     assert all(torch.equal(a, b) for a, b in zip(*(r[3:] for r in runs)))
     if bits == 8:
         assert runs[1][1][at].isnan().all() and runs[1][2][at].isnan().all()
+
+
+@gpu
+def test_adamw_checks_its_step_state(sbn_lib, cuda_ok):
+    sbn = _sbn()
+    p, g = torch.ones(300, device="cuda"), [torch.ones(300, device="cuda")]
+    opt = sbn.AdamW([p])
+    for err, other in ((ValueError, torch.zeros(2, dtype=torch.int32)), (TypeError, torch.zeros(2, dtype=torch.int64, device="cuda")),
+                       (ValueError, torch.zeros(1, dtype=torch.int32, device="cuda")),
+                       (ValueError, torch.zeros(4, dtype=torch.int32, device="cuda")[::2])):
+        with pytest.raises(err):
+            opt.step_state = other
+    opt.step_state = mine = torch.tensor([41, 0], dtype=torch.int32, device="cuda")
+    opt.step(g)
+    clean(sbn)
+    assert mine.tolist() == [42, 0] and opt.state_dict()["step"].tolist() == [42, 0]
