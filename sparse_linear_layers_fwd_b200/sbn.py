@@ -304,6 +304,8 @@ def quantize_acts(x: torch.Tensor, out_q: Optional[torch.Tensor] = None,
         out_q = torch.empty((t, k), dtype=torch.int8, device=x.device)
     if out_s is None:
         out_s = torch.empty((t,), dtype=torch.float32, device=x.device)
+    if t == 0:
+        return out_q, out_s
     st = lib().sbn_quantize_acts(_ptr(x), t, k, _ptr(out_q), _ptr(out_s), _stream_ptr(stream))
     _check(st, "sbn_quantize_acts")
     return out_q, out_s
@@ -515,7 +517,7 @@ def _need_shape(t: Optional[torch.Tensor], dtype, shape, what: str):
 
 
 def _apart(z: Optional[torch.Tensor], *others: Optional[torch.Tensor]):
-    if z is not None and any(o is not None and o.data_ptr() == z.data_ptr() for o in others):
+    if z is not None and z.numel() and any(o is not None and o.data_ptr() == z.data_ptr() for o in others):
         raise ValueError("out_z must not be another tensor of the call")
 
 
@@ -547,6 +549,12 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
 
 
+def _zero(t: torch.Tensor, stream) -> torch.Tensor:
+    """Zeros in `t` on the call's stream: the gradient of no rows."""
+    with _alloc_on(t.device, stream):
+        return t.zero_()
+
+
 def _scratch(need: int, workspace, like: torch.Tensor, stream):
     if workspace is None:
         return _new((need,), torch.uint8, like, stream) if need else None
@@ -574,6 +582,8 @@ def bitlinear_act(xq: torch.Tensor, s: torch.Tensor, w: PackedWeights, bias: Opt
                   act: str = "none", residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                   out_z: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
     """sbn_bitlinear_act: y = f(z) + residual with z = acc gamma s_t / 127 + bias.
+    T may be 0 in this and the following calls (nothing is enqueued, sums and
+    weight gradients are zeros).
 
     act: "none", "relu", "relu2", "silu" or "gelu". bias: fp32 [N_out];
     residual: bf16 [T, N_out], may be `out` itself. out_z, if given, receives z
@@ -586,6 +596,8 @@ def bitlinear_act(xq: torch.Tensor, s: torch.Tensor, w: PackedWeights, bias: Opt
     _one_device(xq, s)
     code = _act(act)
     out = _act_buffers(xq, t, w, (), bias, residual, out, out_z, stream)
+    if t == 0:
+        return out
     ws = None
     if workspace is not False:
         ws = _scratch(bitlinear_workspace_bytes(t, k, w.n_out), workspace, xq, stream)
@@ -611,6 +623,8 @@ def bitlinear_x_act(x: torch.Tensor, w: PackedWeights, bias: Optional[torch.Tens
     _need_shape(out_s, torch.float32, (t,), "out_s")
     _one_device(x, out_q, out_s)
     out = _act_buffers(x, t, w, (), bias, residual, out, out_z, stream)
+    if t == 0:
+        return out
     args = (_ptr(x), t, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code,
             _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s))
     _run_with_scratch(x, "sbn_bitlinear_x_act", stream, t <= 16, workspace,
@@ -640,6 +654,10 @@ def act_grad(dy: torch.Tensor, z: torch.Tensor, act: str, offsets: Optional[torc
     dbias = None if out_bias is False else out_bias
     _need_shape(dbias, torch.float32, lead + (n_out,), "out_bias")
     _one_device(dy, z, offsets, out, dbias)
+    if rows == 0:
+        if dbias is not None:
+            _zero(dbias, stream)
+        return out, dbias
     if out.data_ptr() == z.data_ptr():
         raise ValueError("out must not be z")
     _run_on(dy.device, "sbn_act_grad", stream, _ptr(dy), _ptr(z), rows, _ptr(offsets), experts, n_out, code, _ptr(out),
@@ -720,6 +738,8 @@ def bitlinear_grouped(xq: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor, 
     _one_device(xq, s, offsets)
     code = _act(act)
     out = _act_buffers(xq, rows, w, (w.experts,), bias, residual, out, out_z, stream)
+    if rows == 0:
+        return out
     _run_on(xq.device, "sbn_bitlinear_grouped", stream, _ptr(xq), _ptr(s), rows, _ptr(offsets), w.experts, k, w.n_out,
             w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z),
             _ptr(out))
@@ -746,6 +766,8 @@ def bitlinear_grouped_x(x: torch.Tensor, offsets: torch.Tensor, w: PackedExperts
     _one_device(x, offsets, out_q, out_s)
     code = _act(act)
     out = _act_buffers(x, rows, w, (w.experts,), bias, residual, out, out_z, stream)
+    if rows == 0:
+        return out
     args = (_ptr(x), rows, _ptr(offsets), w.experts, k, w.n_out, w.n, w.m, _ptr(w.codes), _ptr(w.meta),
             _ptr(w.gamma), _ptr(bias), code, _ptr(residual), _ptr(out_z), _ptr(out), _ptr(out_q), _ptr(out_s))
     _run_with_scratch(x, "sbn_bitlinear_grouped_x", stream, rows <= 16, workspace,
@@ -768,6 +790,8 @@ def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedE
     _one_device(dy, offsets, out)
     if out is None:
         out = _new((rows, w.k), torch.bfloat16, dy, stream)
+    if rows == 0:
+        return out
     ws = _scratch(int(lib().sbn_bitlinear_grouped_grad_x_workspace_bytes(rows, n_out)), workspace, dy, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_x", stream, _ptr(dy), rows, _ptr(offsets), w.experts, w.k, n_out,
             w.n, w.m, _ptr(w.codes), _ptr(w.meta), _ptr(w.gamma), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel())
@@ -791,6 +815,8 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
     _one_device(dy, xq, s, offsets, out)
     if out is None:
         out = _new((experts, n_out, k), torch.bfloat16, dy, stream)
+    if rows == 0:
+        return _zero(out, stream)
     need = int(lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, experts, k, n_out))
     ws = _scratch(need, workspace, dy, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_w", stream, _ptr(dy), _ptr(xq), _ptr(s), rows, _ptr(offsets),

@@ -195,3 +195,42 @@ def test_adamw_checks_its_step_state(sbn_lib, cuda_ok):
     opt.step(g)
     clean(sbn)
     assert mine.tolist() == [42, 0] and opt.state_dict()["step"].tolist() == [42, 0]
+
+
+@gpu
+@pytest.mark.parametrize("side", [False, True])
+@pytest.mark.parametrize("nm", [(6, 8), (2, 4)])
+def test_no_rows(sbn_lib, cuda_ok, nm, side):
+    """A batch without rows runs through a whole block and its backward: empty
+    outputs, and zeros where the sums run over no rows; the checks stay."""
+    sbn = _sbn()
+    n, m = nm
+    E, d, f = 3, 256, 129
+    g = torch.Generator(device="cuda").manual_seed(1)
+    up = sbn.quantize_experts((0.02 * torch.randn(E, f, d, device="cuda", generator=g)).to(torch.bfloat16), n, m)
+    x = torch.empty(0, d, dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream() if side else None
+    new = lambda c, dt: torch.empty(0, c, dtype=dt, device="cuda")  # noqa: E731
+    z, dy, bias = new(f, torch.bfloat16), new(f, torch.bfloat16), torch.zeros(E, f, device="cuda")
+    q, s = sbn.quantize_acts(x, stream=stream)
+    assert q.shape == (0, d) and s.shape == (0,)
+    kw = dict(act="gelu", residual=new(f, torch.bfloat16), out_z=z, stream=stream)
+    ys = [sbn.bitlinear_grouped(q, s, o, up, bias=bias, **kw), sbn.bitlinear_grouped_x(x, o, up, bias=bias, **kw),
+          sbn.bitlinear_act(q, s, up.expert(0), bias=bias[0], **kw), sbn.bitlinear_x_act(x, up.expert(0), bias=bias[0], **kw)]
+    assert all(y.shape == (0, f) and y.dtype == torch.bfloat16 for y in ys)
+    db, dw = torch.full((E, f), 3.0, device="cuda"), torch.full((E, f, d), 3.0, device="cuda").to(torch.bfloat16)
+    torch.cuda.synchronize()
+    dz, sums = sbn.act_grad(dy, z, "gelu", offsets=o, out_bias=db, stream=stream)
+    _, plain = sbn.act_grad(dy, z, "gelu", stream=stream)
+    _, none = sbn.act_grad(dy, z, "gelu", out_bias=False, stream=stream)
+    dx = sbn.bitlinear_grouped_grad_x(dz, o, up, stream=stream)
+    assert sbn.bitlinear_grouped_grad_w(dz, q, s, o, out=dw, stream=stream) is dw
+    fresh = sbn.bitlinear_grouped_grad_w(dz, q, s, o, stream=stream)
+    clean(sbn)
+    assert dz.shape == (0, f) and dx.shape == (0, d) and sums is db and none is None and plain.shape == (f,)
+    assert not db.any() and not plain.any() and not dw.any() and not fresh.any() and fresh.shape == (E, f, d)
+    with pytest.raises(ValueError):
+        sbn.bitlinear_grouped(q, s, o[:2], up)
+    with pytest.raises(ValueError):
+        sbn.bitlinear_grouped_grad_w(dz, q, s, o, out=dw[:1])
