@@ -14,6 +14,7 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -521,8 +522,18 @@ def _apart(z: Optional[torch.Tensor], *others: Optional[torch.Tensor]):
         raise ValueError("out_z must not be another tensor of the call")
 
 
-def _need_packed(w, dev: torch.device):
+@functools.lru_cache(maxsize=256)
+def _row_bytes(k: int, n: int, m: int):
+    return codes_row_bytes(k, n, m), meta_row_bytes(k, n, m)
+
+
+def _need_packed(w, layers: int, dev: torch.device):
+    """The packed arrays of `layers` layers are as large as the sizes beside them say."""
     c, m, g = w.codes, w.meta, w.gamma
+    cr, mr = _row_bytes(w.k, w.n, w.m)
+    rows = layers * w.n_out
+    if c.nbytes != rows * cr or g.nbytes != 4 * layers or (m is not None and mr and m.nbytes != rows * mr):
+        raise ValueError(f"the packed arrays are not those of {layers} layer(s) of {w.n_out} x {w.k} at {w.n}:{w.m}")
     if c.device != dev or g.device != dev or (m is not None and m.device != dev):
         raise ValueError(f"the packed weights must be on {dev}")
     if not (c.is_contiguous() and g.is_contiguous() and (m is None or m.is_contiguous())):
@@ -531,7 +542,7 @@ def _need_packed(w, dev: torch.device):
 
 def _act_buffers(x, rows: int, w, lead, bias, residual, out, out_z, stream):
     """Checks of the epilogue's tensors; the output, allocated if not given."""
-    _need_packed(w, x.device)
+    _need_packed(w, lead[0] if lead else 1, x.device)
     _need_shape(bias, torch.float32, lead + (w.n_out,), "bias")
     _need_shape(residual, torch.bfloat16, (rows, w.n_out), "residual")
     _need_shape(out, torch.bfloat16, (rows, w.n_out), "out")
@@ -786,7 +797,7 @@ def bitlinear_grouped_grad_x(dy: torch.Tensor, offsets: torch.Tensor, w: PackedE
     if _experts_of(offsets) != w.experts:
         raise ValueError("offsets and weights differ in experts")
     _need_shape(out, torch.bfloat16, (rows, w.k), "out")
-    _need_packed(w, dy.device)
+    _need_packed(w, w.experts, dy.device)
     _one_device(dy, offsets, out)
     if out is None:
         out = _new((rows, w.k), torch.bfloat16, dy, stream)

@@ -234,3 +234,31 @@ def test_no_rows(sbn_lib, cuda_ok, nm, side):
         sbn.bitlinear_grouped(q, s, o[:2], up)
     with pytest.raises(ValueError):
         sbn.bitlinear_grouped_grad_w(dz, q, s, o, out=dw[:1])
+
+
+@gpu
+def test_packed_arrays_of_other_sizes_are_refused(sbn_lib, cuda_ok):
+    """A handle whose arrays do not belong to the sizes beside them would be
+    read out of range, a set of experts in a layer's place as its first."""
+    from dataclasses import replace
+    sbn = _sbn()
+    layer = Packed(3, 64, 256, 6, 8, "sizes")
+    we, w = layer.packed, layer.packed.expert(0)
+    x, q, s = acts_of(20, 256, "sizes")
+    o = torch.tensor([0, 5, 5, 20], dtype=torch.int32, device="cuda")
+    dy = torch.zeros(20, 64, dtype=torch.bfloat16, device="cuda")
+    single = [lambda h: sbn.bitlinear_act(q, s, h), lambda h: sbn.bitlinear_x_act(x, h)]
+    grouped = [lambda h: sbn.bitlinear_grouped(q, s, o, h), lambda h: sbn.bitlinear_grouped_x(x, o, h),
+               lambda h: sbn.bitlinear_grouped_grad_x(dy, o, h)]
+    for calls, good, others in ((single, w, [we]), (grouped, we, [replace(we, gamma=w.gamma)])):
+        half = good.codes.flatten()[:good.codes.numel() // 2]
+        others += [replace(good, codes=half), replace(good, meta=good.meta.flatten()[16:]), replace(good, n=4),
+                   replace(good, gamma=good.gamma.to(torch.bfloat16))]
+        for call in calls:
+            call(good)
+            for h in others:
+                with pytest.raises(ValueError):
+                    call(h)
+            with pytest.raises(sbn.SbnError):
+                call(replace(good, meta=None))
+    clean(sbn)
