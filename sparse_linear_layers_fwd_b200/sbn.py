@@ -900,23 +900,33 @@ class AdamW:
         self._table[7::8] = array.array("q", self._sizes)
         st = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
         like = self.params[0]
-        self.m = [like.new_zeros(n, dtype=st) for n in self._sizes]
-        self.v = [like.new_zeros(n, dtype=st) for n in self._sizes]
+        self.m, self.v = (self._filled(like.new_zeros, st, self._sizes) for _ in "mv")
         if state_bits == 8:
-            self.m_scales = [like.new_ones(-(-n // ADAMW_BLOCK), dtype=torch.float32) for n in self._sizes]
-            self.v_scales = [like.new_ones(-(-n // ADAMW_BLOCK), dtype=torch.float32) for n in self._sizes]
+            self.m_scales, self.v_scales = (self._filled(like.new_ones, torch.float32, self._scale_sizes()) for _ in "mv")
         self.step_state = like.new_zeros(2, dtype=torch.int32)
+
+    @staticmethod
+    def _filled(new, dtype, sizes) -> list:
+        """A tensor of every size, parts of one buffer from `new` (one fill for
+        all of them) that start on multiples of ADAMW_BLOCK elements."""
+        cuts = [c for n in sizes for c in (n, -n % ADAMW_BLOCK)]
+        return list(torch.split_with_sizes(new(sum(cuts), dtype=dtype), cuts)[::2])
 
     def _own(self, column: int, tensors, dtype, sizes) -> tuple:
         """State tensors of one kind, checked, their addresses put into the table."""
         tensors = tuple(tensors)
-        for t in tensors:
-            _need(t, dtype, "state")
-        if [t.numel() for t in tensors] != sizes:
-            raise ValueError("a state tensor differs from its parameter in size")
-        _one_device(self.params[0], *tensors)
-        self._table[column::8] = array.array("q", [t.data_ptr() for t in tensors])
+        self._need_like_params(tensors, dtype, sizes, "state")
+        self._table[column::8] = array.array("q", map(torch.Tensor.data_ptr, tensors))
         return tensors
+
+    def _need_like_params(self, tensors, dtype, sizes, what: str):
+        """Checks of one contiguous tensor for every parameter, all at once."""
+        if (list(map(torch.Tensor.numel, tensors)) != sizes or not all(map(torch.Tensor.is_contiguous, tensors))
+                or set(map(_dtype_of, tensors)) != {dtype}
+                or set(map(torch.Tensor.get_device, tensors)) != {self.device.index}):
+            for t in tensors:
+                _need(t, dtype, what)
+            raise ValueError(f"a {what} differs from its parameter in size or device")
 
     def _state_dtype(self):
         return torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
@@ -969,11 +979,7 @@ class AdamW:
         gd = grads[0].dtype
         if gd not in (torch.float32, torch.bfloat16):
             raise TypeError(f"grads must be float32 or bfloat16, got {gd}")
-        if (list(map(torch.Tensor.numel, grads)) != self._sizes or not all(map(torch.Tensor.is_contiguous, grads))
-                or set(map(_dtype_of, grads)) != {gd} or set(map(torch.Tensor.get_device, grads)) != {self.device.index}):
-            for g in grads:
-                _need(g, gd, "grads")
-            raise ValueError("a gradient differs from its parameter in size or device")
+        self._need_like_params(grads, gd, self._sizes, "gradient")
         lr_dev = None
         lr = self.lr
         for t, what in ((lr if isinstance(lr, torch.Tensor) else None, "lr"), (grad_scale, "grad_scale")):

@@ -262,3 +262,31 @@ def test_packed_arrays_of_other_sizes_are_refused(sbn_lib, cuda_ok):
             with pytest.raises(sbn.SbnError):
                 call(replace(good, meta=None))
     clean(sbn)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_states_take_one_fill_a_kind(sbn_lib, cuda_ok, bits):
+    """A new optimizer fills one buffer for each kind of state, whatever the
+    number of tensors; its parts are apart and aligned for the wide accesses,
+    and a step gives what states of their own give."""
+    sbn = _sbn()
+    sizes = [1, 256, 0, 257, 5000, 7]
+    g = torch.Generator(device="cuda").manual_seed(2)
+    p = [torch.randn(n, device="cuda", generator=g) for n in sizes]
+    grads = [torch.randn(n, device="cuda", generator=g) for n in sizes]
+    one, own = sbn.AdamW([x.clone() for x in p], state_bits=bits), sbn.AdamW([x.clone() for x in p], state_bits=bits)
+    kinds = [one.m, one.v] + ([one.m_scales, one.v_scales] if bits == 8 else [])
+    assert len({t.untyped_storage().data_ptr() for kind in kinds for t in kind if t.numel()}) == len(kinds)
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for kind in kinds for t in kind if t.numel())
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:])) and all(a % 32 == 0 for a, _ in spans)
+    assert not any(t.float().any() for t in one.m + one.v) and all((t == 1).all() for kind in kinds[2:] for t in kind)
+    own.m, own.v = [t.clone() for t in own.m], [t.clone() for t in own.v]
+    if bits == 8:
+        own.m_scales, own.v_scales = [t.clone() for t in own.m_scales], [t.clone() for t in own.v_scales]
+    for opt in (one, own):
+        opt.step(grads)
+        opt.step(grads)
+    clean(sbn)
+    for a, b in ((one.params, own.params), (one.m, own.m), (one.v, own.v)):
+        assert all(torch.equal(x.float(), y.float()) for x, y in zip(a, b))
