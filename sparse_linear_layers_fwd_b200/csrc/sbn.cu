@@ -522,15 +522,22 @@ sbn_status launch_tc2(const CUtensorMap& tm, const CUtensorMap& tw, const CUtens
 // per-stage cost in the MMA thread) counted as 0.6 of a 256-token one. The
 // narrow tiles win where the wide ones leave pairs idle (few tiles, or a
 // short last wave).
-// With an epilogue (epi) the epilogue sets the pace, and a narrow tile costs
-// half a wide one (2048 x 4864, K = 896: 5 rounds of narrow tiles against 3 of
-// wide ones).
+// With an epilogue (epi) a narrow tile costs 0.55 of a wide one, and its first
+// load and last epilogue, which nothing hides, a fifth of a wide tile less.
+// Both tiles measured at T = 64 to 6000, K = 512 to 6912, N_out = 896 to 8192,
+// without an activation, with relu2, gelu and silu, with and without residual
+// and z (810 points): narrow tiles take 0.64 to 0.84 of the time where both need
+// one round, 0.84 to 1.01 for two rounds against one, 0.83 to 0.94 for three
+// against two, 0.88 to 0.97 for five against three, 0.97 to 1.09 for six against
+// three, 0.98 to 1.14 for twelve against six. This rule loses 0.2 % to the better
+// of the two in the mean and 7 % at most (14 rounds against 8 at K = 4096);
+// narrow tiles wherever they need fewer than twice the rounds lost 1.8 % and 19 %.
 bool tc2_narrow_pays(int t, int n_out, int wide_pairs, int narrow_pairs, bool epi) {
   if (narrow_pairs <= 0) return false;
   const long long rp = (n_out + 255) / 256;
   const long long wide = rp * ((t + 255) / 256), narrow = rp * ((t + 127) / 128);
   const long long rw = (wide + wide_pairs - 1) / wide_pairs, rn = (narrow + narrow_pairs - 1) / narrow_pairs;
-  return epi ? rn < 2 * rw : 6 * rn < 10 * rw;
+  return epi ? 11 * rn < 20 * rw + 4 : 6 * rn < 10 * rw;
 }
 
 // 2:4 weights on the sparse tensor-core MMA: expanded once into the
