@@ -73,18 +73,6 @@ SBN_DEVFN bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t* bar2, ui
   return __all_sync(0xffffffffu, mbar_wait_lane(bar, parity) && mbar_wait_lane(bar2, parity2));
 }
 
-// One non-blocking probe of the phase of the given parity (no suspension,
-// no time bound): true if it has completed. Callers fall back to mbar_wait.
-SBN_DEVFN bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // True in one lane of the warp (all lanes must call it).
 SBN_DEVFN bool elect_one() {
   uint32_t p;
