@@ -290,3 +290,90 @@ def test_adamw_states_take_one_fill_a_kind(sbn_lib, cuda_ok, bits):
     clean(sbn)
     for a, b in ((one.params, own.params), (one.m, own.m), (one.v, own.v)):
         assert all(torch.equal(x.float(), y.float()) for x, y in zip(a, b))
+
+
+@gpu
+@pytest.mark.parametrize("k,n_out,n,m,sizes,tail", [
+    (384, 257, 6, 8, (70, 0, 1, 64, 65), 3), (256, 136, 2, 4, (5, 0, 0, 3), 0), (640, 1000, 8, 16, (129, 300), 7), (128, 9, 8, 8, (1,), 0)])
+def test_canaries_of_gradient_workspaces(sbn_lib, cuda_ok, k, n_out, n, m, sizes, tail):
+    """Workspaces of exactly the reported size, with known bytes on both sides:
+    dX's pitched copy of dY, dW's three arrays, the expanded weights; and the
+    outputs of act_grad."""
+    from test_canaries import Guarded
+    sbn = _sbn()
+    E, rows = len(sizes), sum(sizes) + tail
+    layer = Packed(E, n_out, k, n, m, "guard")
+    x, q, s = acts_of(rows, k, f"guard{k}")
+    o = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    dy = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
+    z = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
+    gd = Guarded()
+    need_x = int(sbn.lib().sbn_bitlinear_grouped_grad_x_workspace_bytes(rows, n_out))
+    need_w = int(sbn.lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, E, k, n_out))
+    assert (need_x > 0) == (n_out % 8 != 0) and need_w > 0
+    dx, dw = gd.tensor((rows, k), torch.bfloat16), gd.tensor((E, n_out, k), torch.bfloat16)
+    sbn.bitlinear_grouped_grad_x(dy, o, layer.packed, out=dx, workspace=gd.tensor((need_x,), torch.uint8) if need_x else None)
+    sbn.bitlinear_grouped_grad_w(dy, q, s, o, out=dw, workspace=gd.tensor((need_w,), torch.uint8))
+    need = sbn.bitlinear_workspace_bytes(rows, k, n_out)
+    sbn.bitlinear_act(q, s, layer.packed.expert(0), act="silu", residual=dy, out=gd.tensor((rows, n_out), torch.bfloat16),
+                      out_z=gd.tensor((rows, n_out), torch.bfloat16), workspace=gd.tensor((need,), torch.uint8) if need else None)
+    sbn.act_grad(dy, z, "gelu", offsets=o, out=gd.tensor((rows, n_out), torch.bfloat16), out_bias=gd.tensor((E, n_out), torch.float32))
+    gd.check()
+    inside = slice(0, rows - tail)
+    assert torch.equal(dx[inside], sbn.bitlinear_grouped_grad_x(dy, o, layer.packed)[inside])
+    assert torch.equal(dw, sbn.bitlinear_grouped_grad_w(dy, q, s, o))
+    clean(sbn)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("sizes", [(1, 255, 257, 5000, 8), (3,) * 30])
+def test_canaries_of_adamw(sbn_lib, cuda_ok, bits, sizes):
+    """Parameters, bf16 copies, states and scales with known bytes around each."""
+    from test_canaries import Guarded
+    sbn = _sbn()
+    gd = Guarded()
+    state = torch.float32 if bits == 32 else torch.float8_e4m3fn
+
+    def zeros(n, dtype):
+        t = gd.tensor((n,), dtype)
+        t.view(torch.uint8).zero_()
+        return t
+    p, c = [zeros(n, torch.float32) for n in sizes], [zeros(n, torch.bfloat16) for n in sizes]
+    opt = sbn.AdamW(p, copies=c, state_bits=bits)
+    opt.m, opt.v = [zeros(n, state) for n in sizes], [zeros(n, state) for n in sizes]
+    if bits == 8:
+        opt.m_scales = [zeros(-(-n // 256), torch.float32) for n in sizes]
+        opt.v_scales = [zeros(-(-n // 256), torch.float32) for n in sizes]
+    opt.step_state = zeros(2, torch.int32)
+    grads = [torch.ones(n, device="cuda") for n in sizes]
+    opt.step(grads)
+    opt.step(grads)
+    gd.check()
+    assert all(bool((t < 0).all()) for t in p + c) and opt.step_state.tolist() == [2, 0]
+
+
+@gpu
+@pytest.mark.parametrize("gdt", [torch.float32, torch.bfloat16])
+def test_adamw_averages_bit_for_bit(sbn_lib, cuda_ok, gdt):
+    """32-bit m and v are the products and sums of the formula, each rounded on
+    its own in fp32 (numpy does the same); the parameters' quotient goes through
+    an approximate reciprocal and has no such property."""
+    sbn = _sbn()
+    f = np.float32
+    n, b1, b2 = 70001, 0.9, 0.95
+    g = torch.Generator(device="cuda").manual_seed(9)
+    p = torch.randn(n, device="cuda", generator=g)
+    opt = sbn.AdamW([p], lr=1e-3, betas=(b1, b2))
+    scale = torch.tensor([0.37], device="cuda")
+    m, v = np.zeros(n, f), np.zeros(n, f)
+    for _ in range(4):
+        grad = (torch.randn(n, device="cuda", generator=g) * torch.exp2(torch.randint(-30, 10, (n,), device="cuda").float())).to(gdt)
+        opt.step([grad], grad_scale=scale)
+        clean(sbn)
+        x = grad.float().cpu().numpy() * f(0.37)
+        m = f(b1) * m + f(1 - b1) * x
+        v = f(b2) * v + f(1 - b2) * (x * x)
+        assert m.dtype == f and v.dtype == f
+        assert np.array_equal(opt.m[0].cpu().numpy(), m) and np.array_equal(opt.v[0].cpu().numpy(), v)
