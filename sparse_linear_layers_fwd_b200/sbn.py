@@ -716,7 +716,9 @@ def quantize_experts(w: torch.Tensor, n: int, m: int, out: Optional[PackedExpert
             workspace = torch.empty(workspace_bytes(n_out, k), dtype=torch.uint8, device=w.device)
     if (out.experts, out.n_out, out.k, out.n, out.m) != (experts, n_out, k, n, m):
         raise ValueError("out describes other experts")
-    _one_device(w, out.codes, workspace)
+    _need_packed(out, experts, w.device)
+    _need(workspace, torch.uint8, "workspace")
+    _one_device(w, workspace)
     for e in range(experts):
         p = out.expert(e)
         _run_on(w.device, "sbn_quantize_weights", stream, _ptr(w[e]), n_out, k, n, m, _ptr(p.codes), _ptr(p.meta),

@@ -377,3 +377,24 @@ def test_adamw_averages_bit_for_bit(sbn_lib, cuda_ok, gdt):
         v = f(b2) * v + f(1 - b2) * (x * x)
         assert m.dtype == f and v.dtype == f
         assert np.array_equal(opt.m[0].cpu().numpy(), m) and np.array_equal(opt.v[0].cpu().numpy(), v)
+
+
+@gpu
+def test_quantize_experts_checks_what_it_writes(sbn_lib, cuda_ok):
+    from dataclasses import replace
+    sbn = _sbn()
+    w = torch.randn(3, 64, 256, device="cuda").to(torch.bfloat16)
+    out = sbn.alloc_experts(3, 64, 256, 6, 8, "cuda")
+    for bad in (replace(out, codes=out.codes[:2]), replace(out, meta=out.meta[:2]), replace(out, gamma=out.gamma[:1]),
+                replace(out, codes=torch.empty(3, 64, 2 * out.codes.shape[2], dtype=torch.uint8, device="cuda")[..., ::2]),
+                replace(out, gamma=out.gamma.cpu())):
+        with pytest.raises(ValueError):
+            sbn.quantize_experts(w, 6, 8, out=bad)
+    with pytest.raises(TypeError):
+        sbn.quantize_experts(w, 6, 8, out=out, workspace=torch.empty(1 << 16, device="cuda"))
+    with pytest.raises(ValueError):
+        sbn.quantize_experts(w, 6, 8, out=out, workspace=torch.empty(1 << 18, dtype=torch.uint8))
+    assert sbn.quantize_experts(w, 6, 8, out=out) is out
+    again = sbn.quantize_experts(w, 6, 8)
+    clean(sbn)
+    assert all(torch.equal(a, b) for a, b in ((out.codes, again.codes), (out.meta, again.meta), (out.gamma, again.gamma)))
