@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_feedforward import acts_of, clean, close, epilogue_inputs, reference
+from test_feedforward import H, U, acts_of, clean, close, dw_reference, epilogue_inputs, reference
 
 gpu = pytest.mark.gpu
 
@@ -15,6 +15,22 @@ SMEM = 227 * 1024    # shared memory of a CTA
 def _sbn():
     from sparse_linear_layers_fwd_b200 import sbn
     return sbn
+
+
+class Repeated:
+    """`experts` experts that share the weights of a few layers: expert e has
+    those of layer e modulo their number."""
+
+    def __init__(self, few, experts):
+        sbn = _sbn()
+        p, pick = few.packed, torch.arange(experts, device="cuda") % few.packed.experts
+        self.packed = sbn.PackedExperts(p.codes[pick], None if p.meta is None else p.meta[pick], p.gamma[pick], p.n_out, p.k,
+                                        p.n, p.m, experts)
+        self.gamma = few.gamma[pick]
+
+        class Dense(list):
+            shape = (experts, p.n_out, p.k)
+        self.dense = Dense(few.dense[i] for i in pick.tolist())
 
 
 class Packed:
@@ -398,3 +414,123 @@ def test_quantize_experts_checks_what_it_writes(sbn_lib, cuda_ok):
     again = sbn.quantize_experts(w, 6, 8)
     clean(sbn)
     assert all(torch.equal(a, b) for a, b in ((out.codes, again.codes), (out.meta, again.meta), (out.gamma, again.gamma)))
+
+
+def run_spans(sizes):
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    return torch.tensor(off, dtype=torch.int32, device="cuda"), list(zip(off[:-1].tolist(), off[1:].tolist()))
+
+
+@gpu
+@pytest.mark.parametrize("k,n_out", [(128, 1416), (1280, 24)])
+def test_more_tiles_than_a_list_holds(sbn_lib, cuda_ok, k, n_out):
+    """1000 experts of one or two rows: a CTA of the forward (K = 128) or of dX
+    (K = 1280) has more tiles than its list of 64 or 32 worked out ahead."""
+    sbn = _sbn()
+    E = 1000
+    sizes = [1 + e % 2 for e in range(E)]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert E * ((n_out + 127) // 128) // sms > 64 or E * ((k + 255) // 256) // sms > 32
+    layer = Repeated(Packed(3, n_out, k, 6, 8, "list"), E)
+    o, spans = run_spans(sizes)
+    rows = sum(sizes)
+    x, q, s = acts_of(rows, k, f"list{k}")
+    bias, res = epilogue_inputs(rows, n_out, E)
+    y, ytol, z, ztol = reference(layer, q, s, spans, bias, "gelu", res)
+    oz = torch.empty(rows, n_out, dtype=torch.bfloat16, device="cuda")
+    close(sbn.bitlinear_grouped(q, s, o, layer.packed, bias=bias, act="gelu", residual=res, out_z=oz), y, ytol, "y")
+    close(oz, z, ztol, "z")
+    dy = res
+    dx, dw = sbn.bitlinear_grouped_grad_x(dy, o, layer.packed), sbn.bitlinear_grouped_grad_w(dy, q, s, o)
+    clean(sbn)
+    xd = q.double() * s.double()[:, None] / 127
+    for e, (a, b) in enumerate(spans):
+        d, wd = dy[a:b].double(), layer.dense[e] * layer.gamma[e]
+        ref, mag = d @ wd, d.abs() @ wd.abs()
+        close(dx[a:b], ref, H * ref.abs() + (1 + H) * (2 * n_out + 4) * U * mag, f"dx {e}")
+        close(dw[e], *dw_reference(d, xd[a:b]), f"dw {e}")
+
+
+@gpu
+@pytest.mark.parametrize("rows", [12, 400])
+def test_weights_past_32_bits(sbn_lib, cuda_ok, rows):
+    """300 experts of 2048 x 4096: 2.5e9 weights, so the last experts' dW lies
+    past 2^32 bytes and 2^31 elements. Rows in the first, one in the middle and the
+    last two experts; the others' dW are zeros."""
+    sbn = _sbn()
+    E, n_out, k = 300, 2048, 4096
+    layer = Repeated(Packed(2, n_out, k, 6, 8, "far"), E)
+    sizes = [0] * E
+    for e, part in ((0, 1), (171, 5), (298, 2), (299, 4)):
+        sizes[e] = rows * part // 12
+    o, spans = run_spans(sizes)
+    rows = sum(sizes)
+    x, q, s = acts_of(rows, k, f"far{rows}")
+    active = [e for e in range(E) if sizes[e]]
+    y = sbn.bitlinear_grouped(q, s, o, layer.packed, act="silu")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dy = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
+    dx, dw = sbn.bitlinear_grouped_grad_x(dy, o, layer.packed), sbn.bitlinear_grouped_grad_w(dy, q, s, o)
+    clean(sbn)
+
+    class One:   # the active experts alone
+        dense, gamma = [layer.dense[e] for e in active], layer.gamma[active]
+    one = One()
+
+    class Dense(list):
+        shape = (len(active), n_out, k)
+    one.dense = Dense(one.dense)
+    ref, tol, _, _ = reference(one, q, s, [spans[e] for e in active], None, "silu", None)
+    close(y, ref, tol, "y")
+    xd = q.double() * s.double()[:, None] / 127
+    for e in active:
+        a, b = spans[e]
+        d, wd = dy[a:b].double(), layer.dense[e] * layer.gamma[e]
+        ref, mag = d @ wd, d.abs() @ wd.abs()
+        close(dx[a:b], ref, H * ref.abs() + (1 + H) * (2 * n_out + 4) * U * mag, f"dx {e}")
+        close(dw[e], *dw_reference(d, xd[a:b]), f"dw {e}")
+        dw[e].zero_()
+    assert not any(bool(part.any()) for part in dw.split(50))
+
+
+@gpu
+def test_two_streams_at_once(sbn_lib, cuda_ok):
+    """Forward, backward and optimizer steps of two blocks enqueued on two
+    streams without any order between them give what they give alone."""
+    sbn = _sbn()
+    blocks = []
+    for i, (rows, k, n_out, n, m) in enumerate(((14, 512, 2056, 6, 8), (700, 640, 1000, 2, 4))):
+        layer = Packed(4, n_out, k, n, m, f"two{i}")
+        x, q, s = acts_of(rows, k, f"two{i}")
+        o, _ = run_spans([rows // 2, 0, rows // 4, rows - rows // 2 - rows // 4])
+        g = torch.Generator(device="cuda").manual_seed(i)
+        dy = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
+        p = torch.randn(4, n_out, k, device="cuda", generator=g)
+        blocks.append((layer, x, q, s, o, dy, p))
+
+    def step(block, opt, stream):
+        layer, x, q, s, o, dy, _ = block
+        z = torch.empty_like(dy)
+        y = sbn.bitlinear_grouped_x(x, o, layer.packed, act="relu2", residual=dy, out_z=z, stream=stream)
+        d, db = sbn.act_grad(dy, z, "relu2", offsets=o, stream=stream)
+        dx = sbn.bitlinear_grouped_grad_x(d, o, layer.packed, stream=stream)
+        dw = sbn.bitlinear_grouped_grad_w(d, q, s, o, stream=stream)
+        opt.step([dw], stream=stream)
+        return y, z, d, db, dx, dw, sbn.bitlinear_x_act(x, layer.packed.expert(1), act="gelu", residual=dy, stream=stream)
+
+    def opts():
+        return [sbn.AdamW([b[-1].clone()], state_bits=8, seed=2) for b in blocks]
+    alone = opts()
+    want = [[step(b, o, None) for _ in range(5)] for b, o in zip(blocks, alone)]
+    clean(sbn)
+    both, streams = opts(), [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            got[i].append(step(blocks[i], both[i], streams[i]))
+    clean(sbn)
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for x, y in zip(w, g) for a, b in zip(x, y))
+    for a, b in zip(alone, both):
+        assert torch.equal(a.params[0], b.params[0]) and torch.equal(a.v[0].float(), b.v[0].float())
