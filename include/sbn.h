@@ -506,8 +506,10 @@ sbn_status sbn_act_grad(const void* dy_bf16, const void* z_bf16, int32_t rows,
  * sbn_bitlinear_grouped_grad_w: dW_e = sum over e's rows of dY_r^T (Xq_r s_r /
  * 127), [experts, n_out, k] bf16, zero for an expert without rows. Its workspace
  * (16-byte aligned, sbn_bitlinear_grouped_grad_w_workspace_bytes) holds dY s /
- * 127, scaled by a power of two per expert and feature, and Xq as fp16 (11 bits
- * of every term); fp32 sums.
+ * 127, scaled by a power of two per expert and feature, and Xq as fp16: 11 bits
+ * of every term within 2^-29 of the largest |dY s| of its expert and feature, and
+ * smaller ones to 2^-39 of that; fp32 sums. (sbn_bitlinear_grad_w on an expert's
+ * rows keeps 16 bits, for twice the MMAs.)
  * Errors: SBN_ERR_NULL, SBN_ERR_SHAPE, SBN_ERR_PATTERN, SBN_ERR_ALIGN,
  * SBN_ERR_WORKSPACE (before anything is enqueued); SBN_ERR_CUDA.
  */
@@ -547,7 +549,8 @@ size_t sbn_bitlinear_grouped_grad_w_workspace_bytes(int32_t rows, int32_t expert
 /*
  * sbn_adamw -- one AdamW step over many tensors in one launch (decoupled
  * weight decay; "Sparse-BitNet ..." Table 5 trains the latent weights with
- * it). With t = step[0] + 1, per element, every operation rounded in fp32:
+ * it). With t = step[0] + 1, per element, every operation of m and v rounded in
+ * fp32 (p's quotient by an approximate reciprocal, within 2^-22):
  *     m = b1 m + (1 - b1) g        v = b2 v + (1 - b2) g^2
  *     p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
  * and step[0] = t afterwards (on the device, so the call can be captured into
@@ -644,8 +647,9 @@ sbn_status sbn_selftest_wait_timeout(int32_t which, int64_t limit_ns, void* stre
  * sbn_set_programmatic_launch -- library-wide launch setting (no counterpart
  * in the method). Enabled (the default), the kernels of sbn_quantize_acts,
  * of the contraction for T > 16 with a workspace (the weight expansion and
- * the CTA-pair kernel) and of the decode GEMV are launched with CUDA's
- * programmatic stream serialization: such a kernel may be scheduled while
+ * the CTA-pair kernel), of the decode GEMV, of the calls with an epilogue, of
+ * the grouped calls and their gradients, of sbn_act_grad and of sbn_adamw are
+ * launched with CUDA's programmatic stream serialization: such a kernel may be scheduled while
  * the previous kernel on the stream is finishing, and it waits on the device
  * for that kernel to complete before it reads or writes global memory. Outputs are identical
  * either way; only the gaps between kernels change. enable = 0 launches

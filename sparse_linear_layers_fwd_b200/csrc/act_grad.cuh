@@ -11,8 +11,10 @@
 // cluster start and end together, and with eight of them per block of columns a
 // batch over 16 experts ran at a third of the bandwidth. Where N_out is not a
 // multiple of 8 a lane takes every 8th column with 2-byte accesses.
-// Measured at 4096 rows of 6912 features, 16 experts: 32 us, 5.3 TB/s, 82 % of
-// the copy rate; at 509 rows the kernel takes 9 us, the call 13.8.
+// Measured at 4096 rows of 6912 features, 16 experts: 31 to 34 us, 5.0 to 5.5
+// TB/s, 78 to 85 % of the copy rate; at 509 rows the kernel takes 9 us, the call
+// 13.3. 6911 features, by 2-byte accesses: 59 us where 6912 take 29 (captured
+// calls, one after the other).
 #pragma once
 
 #include "common.cuh"
@@ -54,8 +56,8 @@ act_grad_kernel(const AgParams p) {
   int lo = 0, hi = p.grp.rows;
   if (p.grp.offsets) {
     // as grp_build has them: the largest offset so far, so that no row belongs
-    // to two experts whatever the offsets are (every warp for itself: with a
-    // barrier 4096 rows of 16 experts took 36 us, not 32)
+    // to two experts whatever the offsets are (every warp for itself, which saves
+    // a barrier: 31 to 34 us at 4096 rows of 16 experts, 31 to 36 with one)
     const int next = p.grp.offsets[e + 1];
     int top = 0;
     for (int i = tid & 31; i <= e; i += 32) top = max(top, p.grp.offsets[i]);

@@ -8,7 +8,9 @@
 //     m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
 //     p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // every product and sum rounded on its own in fp32 (no fused multiply-add),
-// so that an elementwise evaluation gives the same bits.
+// so that an elementwise evaluation gives the same bits of m and v. p's quotient
+// goes through an approximate reciprocal and the bias corrections through
+// expm1f: p is within 32 half steps of its update.
 //
 // 8-bit states: a block of 256 elements shares one power of two per state;
 // m and r = sqrt(v) are held as e4m3 codes times it. The codes round up with
@@ -25,11 +27,12 @@
 // the segments of 2048 elements of all tensors. The tensor table is a kernel
 // parameter: no copy to the device, nothing to keep alive, and the call can be
 // captured into a graph. 28 bytes per element with an fp32 master, its bf16 copy
-// and fp32 states, 16 with 8-bit states. Measured with 8-bit states at 114
-// million elements (72 tensors): 455 us, 4.0 TB/s, 62 % of the copy rate; bound
-// by instruction issue (about 100 per element: the two roundings, the hash and
-// the blocks' maxima), no longer by DRAM. A step of 24 small tensors takes 6.6
-// us on the device.
+// and fp32 states, 16 with 8-bit states. Measured at 114 million elements (72
+// tensors): 32-bit states 559 us, 5.7 TB/s, 89 % of the copy rate, bound by DRAM;
+// 8-bit states 462 us, 4.0 TB/s, 61 %, bound by instruction issue (74 % of the
+// slots, about 100 instructions per element: the two roundings, the hash and the
+// blocks' maxima). With bf16 parameters 438 and 488 us: there the 8-bit states
+// save memory, not time. A step of 24 small tensors takes 6.6 us on the device.
 #pragma once
 
 #include "common.cuh"

@@ -37,10 +37,12 @@
 // TMEM: two accumulators of 192 columns, so that the epilogue hides behind the
 // next tile, and three A slots of 32 columns (a 128-position block each).
 // Measured at 16384 rows (30 of 32 experts, K = 2048, N_out = 2816, 6:8, with the
-// quantization) and at 256 rows of 64 experts (K = 2048, N_out = 1408, 2:4):
-//   this split                                                136 us, 41.4 us
-//   the even codes masked group by group, not once a span     138 us, 43.2 us
-// (the following with the latter)
+// quantization) and at 256 rows of 64 experts (K = 2048, N_out = 1408, 2:4),
+// whole calls, the inputs changed from call to call:
+//   this split                                         151 to 155 us, 39.1 us
+//   the even codes masked group by group, not once
+//   a span                                             154 to 156 us, 40.2 us
+// On an earlier build that took 138 and 43.2 us on one set of inputs:
 //   160-column accumulators, one ring of three 256-position
 //   stages for both operands                                  153 us, 39 us
 //   one accumulator of 256 columns, its epilogue exposed      150 us, 43.6 us
