@@ -505,11 +505,13 @@ sbn_status sbn_act_grad(const void* dy_bf16, const void* z_bf16, int32_t rows,
  * bytes and NULL for n_out a multiple of 8) holds dY at a pitch of 16 bytes.
  * sbn_bitlinear_grouped_grad_w: dW_e = sum over e's rows of dY_r^T (Xq_r s_r /
  * 127), [experts, n_out, k] bf16, zero for an expert without rows. Its workspace
- * (16-byte aligned, sbn_bitlinear_grouped_grad_w_workspace_bytes) holds dY s /
- * 127, scaled by a power of two per expert and feature, and Xq as fp16: 11 bits
- * of every term within 2^-29 of the largest |dY s| of its expert and feature, and
- * smaller ones to 2^-39 of that; fp32 sums. (sbn_bitlinear_grad_w on an expert's
- * rows keeps 16 bits, for twice the MMAs.)
+ * (16-byte aligned) holds dY s / 127, scaled by a power of two per expert and
+ * feature, and Xq as fp16. With sbn_bitlinear_grouped_grad_w2_workspace_bytes or
+ * more, dY s / 127 is held in two parts: 22 bits of every term, or 2^-39 of the
+ * largest |dY s| of its expert and feature where that is more. With
+ * sbn_bitlinear_grouped_grad_w_workspace_bytes or more, in one part: 11 bits, or
+ * 2^-39, for half the MMAs; sums in which terms cancel then lose what
+ * sbn_bitlinear_grad_w (16 bits) would keep. fp32 sums in both.
  * Errors: SBN_ERR_NULL, SBN_ERR_SHAPE, SBN_ERR_PATTERN, SBN_ERR_ALIGN,
  * SBN_ERR_WORKSPACE (before anything is enqueued); SBN_ERR_CUDA.
  */
@@ -545,6 +547,8 @@ sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq,
                                         void* stream);
 size_t sbn_bitlinear_grouped_grad_w_workspace_bytes(int32_t rows, int32_t experts,
                                                     int32_t k, int32_t n_out);
+size_t sbn_bitlinear_grouped_grad_w2_workspace_bytes(int32_t rows, int32_t experts,
+                                                     int32_t k, int32_t n_out);
 
 /*
  * sbn_adamw -- one AdamW step over many tensors in one launch (decoupled

@@ -30,23 +30,28 @@
 // caller's workspace, as fp16, every expert's rows padded with zeros to a
 // multiple of 64: Xq (exact) and a = dY s / 127 times a power of two per
 // (expert, feature) that brings the largest |a| of the feature just below
-// 2^15. fp16 keeps 11 bits of an a within 2^-29 of that largest, so each
-// product is within 2^-11 of itself, an eighth of the bf16 result's own
-// rounding; bf16 would keep 8 bits, and two bf16 parts (as in bwd_tc.cuh) take
-// twice the MMAs. bwd_dw_grp_kernel then is a plain TMA-fed product over
-// tiles of 128 features x 256 positions, both operands MN-major (features and
+// 2^15. a is held in two fp16 parts, a rounded and what that leaves: together 22
+// bits of it, or 2^-39 of the feature's largest. With one part (11 bits; a
+// workspace of that size) the MMAs are halved: 152 us in place of 189 for dX and dW
+// at 8192 rows, and the error after the rounding of dW to bf16 is the same to
+// 1 % (1.67e-3 against 1.66e-3) - but not where terms cancel: rows in pairs of
+// opposite gradients and nearly the same activations leave 1.5e-2, two parts
+// 1.66e-3, the two bf16 parts of bwd_tc.cuh 1.67e-3. bwd_dw_grp_kernel then is a
+// plain TMA-fed product over tiles of 128 features x 256 positions, two MMAs for
+// every 16 rows into the same accumulator, both operands MN-major (features and
 // positions are contiguous in a row): 1 KB atoms of 8 rows x 64 columns.
 // Converting in the product's own producer warps instead, for every tile
 // again, took six times as long as its MMAs.
 // Its tiles leave through shared memory and TMA stores: from registers, each
-// lane writing its feature's 64 bytes, it took 57 us where it now takes 48.
+// lane writing its feature's 64 bytes, it took 57 us in place of 48 (one part).
 //
 // Where N_out is not a multiple of 8, dY's rows do not start on 16-byte
 // boundaries: dW's preparation reads them two bytes at a time, and dX gets a
 // copy of dY at a padded pitch first (bwd_pitch_kernel).
-// Measured at 8192 rows of 16 experts (K = 2048, N_out = 1408, 6:8): dX 70 us,
-// preparation 31, dW 48 (0.58 of the bf16 rate); at 1000 rows (K = 896, N_out =
-// 1000, 8:16) 18.8, 6.3 and 15.6 us.
+// Measured launch by launch on cold caches at 8192 rows of 16 experts (K = 2048,
+// N_out = 1408, 6:8): dX 72 us, preparation 51 (one part 43), dW 73 (0.76 of the
+// bf16 rate; one part 50); at 1000 rows (K = 896, N_out = 1000, 8:16) 20, 13 and
+// 17.5 us (dW of one part 16.5). Back to back they overlap: 189 and 40 us in all.
 #pragma once
 
 #include <cuda.h>
@@ -374,6 +379,7 @@ struct GwParams {
   uint16_t* a16;
   uint16_t* x16;
   float* scale;
+  long long a_rows; // two parts of a: the padded rows of the first, the second follows; one part: 0
   int cluster;      // CTAs per (expert, 64 columns) in the preparation
   int a_ctas;       // its CTAs that scale dY; the others convert Xq
 };
@@ -475,14 +481,23 @@ __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const GwParams 
       for (int u = 0; u < 4; ++u) {
         const int r = r0 + u * step;
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t h[4];
+        uint32_t h[4], l[4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float a0 = __fmul_rn(__fmul_rn(__uint_as_float(w[j] << 16), sc[u]), mult[2 * j]);
           const float a1 = __fmul_rn(__fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), sc[u]), mult[2 * j + 1]);
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(a1), "f"(a0));
+          if (!p.a_rows) continue;
+          // what the first part leaves, exact in fp32
+          float h0, h1;
+          asm("{\n.reg .f16 x, y;\nmov.b32 {x, y}, %2;\ncvt.f32.f16 %0, x;\ncvt.f32.f16 %1, y;\n}\n" : "=f"(h0), "=f"(h1) : "r"(h[j]));
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(l[j]) : "f"(__fsub_rn(a1, h1)), "f"(__fsub_rn(a0, h0)));
         }
-        if (in && r < pad_hi) *reinterpret_cast<uint4*>(dst + (size_t)(r - lo) * p.Np) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (in && r < pad_hi) {
+          uint16_t* at = dst + (size_t)(r - lo) * p.Np;
+          *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+          if (p.a_rows) *reinterpret_cast<uint4*>(at + (size_t)p.a_rows * p.Np) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
       }
     }
     griddep_launch_dependents();
@@ -528,9 +543,9 @@ __global__ void __launch_bounds__(kGpThreads) bwd_dw_prep_kernel(const GwParams 
 constexpr int kGwBM = 128;                       // features per tile (MMA M)
 constexpr int kGwBN = 256;                       // positions per tile (MMA N)
 constexpr int kGwBK = 64;                        // rows per stage
-constexpr int kGwStages = 4;
-constexpr int kGwABytes = kGwBM * kGwBK * 2;     // 16 KB
-constexpr int kGwStageBytes = kGwABytes + kGwBN * kGwBK * 2;
+constexpr int kGwPart = kGwBM * kGwBK * 2;       // a part of a in a stage, 16 KB
+constexpr int kGwRing = 192 * 1024;              // three stages of two parts, four of one
+constexpr int kGwMaxStages = 4;
 constexpr int kGwThreads = 384;                  // TMA, MMA, list, -, eight epilogue warps
 constexpr int kGwOut = 8 * 2048;                 // a warp's 32 features x 32 positions of dW
 // instruction descriptor: f32 accumulate, fp16 A and B, both MN-major
@@ -538,7 +553,7 @@ constexpr uint32_t kGwIdesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(
                               ((uint32_t)(kGwBM >> 4) << 24);
 
 __host__ __device__ inline size_t gw_smem_bytes(int experts) {
-  return 1024 + (size_t)kGwStages * kGwStageBytes + kGwOut + (2 * kGwStages + 4) * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
+  return 1024 + (size_t)kGwRing + kGwOut + (2 * kGwMaxStages + 4) * 8 + 16 + 2 * 4 * (size_t)(experts + 1);
 }
 
 SBN_DEVFN void tc_mma_f16_gw(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
@@ -549,14 +564,19 @@ SBN_DEVFN void tc_mma_f16_gw(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, ui
       : "memory");
 }
 
-// tmap_a, tmap_x: the fp16 operands, boxes of 64 columns x 64 rows (128-byte swizzle);
-// tmap_dw: dW as [E N, K], boxes of 32 positions x 32 features (64-byte swizzle).
-static __global__ void __launch_bounds__(kGwThreads, 1)
+// tmap_a (the second of two parts p.a_rows rows behind the first), tmap_x: the
+// fp16 operands, boxes of 64 columns x 64 rows (128-byte swizzle); tmap_dw: dW as
+// [E N, K], boxes of 32 positions x 32 features (64-byte swizzle).
+template <int PARTS>
+__global__ void __launch_bounds__(kGwThreads, 1)
 bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_x,
                   const __grid_constant__ CUtensorMap tmap_dw, const GwParams p) {
+  constexpr int kGwABytes = PARTS * kGwPart, kGwStageBytes = kGwABytes + kGwBN * kGwBK * 2;
+  constexpr int kGwStages = kGwRing / kGwStageBytes;
+  static_assert(kGwStages <= kGwMaxStages, "barriers of the ring");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* out = smem + (size_t)kGwStages * kGwStageBytes;
+  uint8_t* out = smem + kGwRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(out + kGwOut);
   uint64_t* empty = full + kGwStages;
   uint64_t* acc_full = empty + kGwStages;   // [2]
@@ -612,7 +632,9 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           // boxes past the last column are zeros
           mbar_arrive_expect_tx(&full[s], (uint32_t)kGwStageBytes);
 #pragma unroll
-          for (int j = 0; j < kGwBM / 64; ++j) tma_load_2d(st + j * 8192, &tmap_a, o0 + 64 * j, row, &full[s]);
+          for (int j = 0; j < PARTS * kGwBM / 64; ++j)
+            tma_load_2d(st + j * 8192, &tmap_a, o0 + 64 * (j % (kGwBM / 64)),
+                        j < kGwBM / 64 ? row : row + (int)p.a_rows, &full[s]);
 #pragma unroll
           for (int j = 0; j < kGwBN / 64; ++j) tma_load_2d(st + kGwABytes + j * 8192, &tmap_x, k0 + 64 * j, row, &full[s]);
         }
@@ -644,9 +666,11 @@ bwd_dw_grp_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         const uint64_t so = (uint64_t)(s * (kGwStageBytes / 16));
         if (lead) {
 #pragma unroll
-          for (int k = 0; k < kGwBK / 16; ++k)   // 16 rows: two 1 KB atom rows of each operand
-            tc_mma_f16_gw(d_tmem, ad0 + so + (uint64_t)(k * (2048 / 16)), bd0 + so + (uint64_t)(k * (2048 / 16)),
-                          (ks > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < PARTS * kGwBK / 16; ++k) {   // 16 rows: two 1 KB atom rows of each operand
+            const int part = k % PARTS, rows16 = k / PARTS;
+            tc_mma_f16_gw(d_tmem, ad0 + so + (uint64_t)((part * kGwPart + rows16 * 2048) / 16),
+                          bd0 + so + (uint64_t)(rows16 * (2048 / 16)), (ks > 0 || k > 0) ? 1u : 0u);
+          }
           tc_commit(&empty[s]);
         }
         __syncwarp();

@@ -49,19 +49,37 @@ struct LaunchDx {
   }
 };
 
-// Workspace of dW: the fp16 operands over padded rows, and the scales.
+// Workspace of dW: the fp16 operands over padded rows (dY s / 127 in one or two
+// parts), and the scales.
 struct GwLayout {
   long long rows;
   int np;
   size_t x16, scale, total;
-  GwLayout(int r, int e, int k, int n) {
+  GwLayout(int r, int e, int k, int n, int parts) {
     rows = gw_padded_rows(r, e);
     np = round_up8(n);
-    x16 = ((size_t)rows * np * 2 + 127) & ~(size_t)127;
+    x16 = ((size_t)parts * rows * np * 2 + 127) & ~(size_t)127;
     scale = x16 + (((size_t)rows * k * 2 + 127) & ~(size_t)127);
     total = scale + round_up16((size_t)e * n * 4);
   }
 };
+
+template <int PARTS>
+sbn_status launch_dw(const GwParams& p, const GwLayout& l, int grid, cudaStream_t st) {
+  const int e = p.grp.experts;
+  CUtensorMap ta, tx, tdw;
+  if (!encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.a16, l.np, (uint64_t)PARTS * l.rows, 2 * (uint64_t)l.np, 64,
+                 kGwBK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.x16, p.K, l.rows, 2 * (uint64_t)p.K, 64, kGwBK,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tdw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.dw, p.K, (uint64_t)e * (uint64_t)p.N, 2 * (uint64_t)p.K, 32, 32,
+                 CU_TENSOR_MAP_SWIZZLE_64B))
+    return SBN_ERR_CUDA;
+  static bool attr_set[kMaxDevices] = {};
+  if (!set_smem_attr_once(bwd_dw_grp_kernel<PARTS>, gw_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
+  return launch_ex(bwd_dw_grp_kernel<PARTS>, dim3((unsigned)grid), dim3(kGwThreads), gw_smem_bytes(e), st, 1, ta, tx, tdw,
+                   p);
+}
 
 sbn_status check_grad(int rows, const int32_t* offsets, int experts, int k, int n_out) {
   if (rows < 1 || n_out < 1 || k < 128 || (k % 128) != 0 || experts < 1 || experts > kGrpMaxExperts) return SBN_ERR_SHAPE;
@@ -109,8 +127,12 @@ sbn_status sbn_bitlinear_grouped_grad_x(const void* dy_bf16, int32_t rows, const
 
 size_t sbn_bitlinear_grouped_grad_w_workspace_bytes(int32_t rows, int32_t experts, int32_t k, int32_t n_out) {
   if (check_grad(rows, nullptr, experts, k, n_out) != SBN_OK) return 0;
-  const GwLayout l(rows, experts, k, n_out);
-  return l.total;
+  return GwLayout(rows, experts, k, n_out, 1).total;
+}
+
+size_t sbn_bitlinear_grouped_grad_w2_workspace_bytes(int32_t rows, int32_t experts, int32_t k, int32_t n_out) {
+  if (check_grad(rows, nullptr, experts, k, n_out) != SBN_OK) return 0;
+  return GwLayout(rows, experts, k, n_out, 2).total;
 }
 
 sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, const float* x_scale, int32_t rows,
@@ -131,9 +153,11 @@ sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, c
   p.dw = reinterpret_cast<uint16_t*>(dw_bf16); p.grp = GrpParams{offsets, experts, rows}; p.K = k; p.N = n_out;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const size_t list = 8 * (size_t)(experts + 1);
-  const GwLayout l(rows, experts, k, n_out);
+  const int parts = ws_bytes >= sbn_bitlinear_grouped_grad_w2_workspace_bytes(rows, experts, k, n_out) ? 2 : 1;
+  const GwLayout l(rows, experts, k, n_out, parts);
   uint8_t* w8 = reinterpret_cast<uint8_t*>(workspace);
   p.Np = l.np;
+  p.a_rows = parts == 2 ? l.rows : 0;
   p.a16 = reinterpret_cast<uint16_t*>(w8);
   p.x16 = reinterpret_cast<uint16_t*>(w8 + l.x16);
   p.scale = reinterpret_cast<float*>(w8 + l.scale);
@@ -150,20 +174,9 @@ sbn_status sbn_bitlinear_grouped_grad_w(const void* dy_bf16, const int8_t* xq, c
   const auto prep = n_out % 8 == 0 ? bwd_dw_prep_kernel<true> : bwd_dw_prep_kernel<false>;
   if ((st = launch_ex(prep, dim3(grid), dim3(kGpThreads), list, cs, (unsigned)p.cluster, p)) != SBN_OK)
     return st;
-  CUtensorMap ta, tx, tdw;
-  if (!encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.a16, l.np, l.rows, 2 * (uint64_t)l.np, 64, kGwBK,
-                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.x16, k, l.rows, 2 * (uint64_t)k, 64, kGwBK,
-                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&tdw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.dw, k, (uint64_t)experts * (uint64_t)n_out,
-                 2 * (uint64_t)k, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-    return SBN_ERR_CUDA;
-  static bool attr_set[kMaxDevices] = {};
-  if (!set_smem_attr_once(bwd_dw_grp_kernel, gw_smem_bytes(kGrpMaxExperts), attr_set)) return SBN_ERR_CUDA;
   const long long tiles = (long long)experts * ((n_out + kGwBM - 1) / kGwBM) * ((k + kGwBN - 1) / kGwBN);
   const int main_grid = (int)std::min(tiles, (long long)sms);
-  return launch_ex(bwd_dw_grp_kernel, dim3((unsigned)main_grid), dim3(kGwThreads), gw_smem_bytes(experts), cs, 1, ta, tx,
-                   tdw, p);
+  return parts == 2 ? launch_dw<2>(p, l, main_grid, cs) : launch_dw<1>(p, l, main_grid, cs);
 }
 
 }  // extern "C"

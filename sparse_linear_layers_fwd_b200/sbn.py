@@ -88,6 +88,7 @@ PROTOTYPES = {
     "sbn_bitlinear_grouped_grad_w": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_p,
                                                     _c_p, _c_sz, _c_p]),
     "sbn_bitlinear_grouped_grad_w_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
+    "sbn_bitlinear_grouped_grad_w2_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32]),
     "sbn_adamw": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, ctypes.c_double, _c_p,
                                  ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _c_p,
                                  ctypes.c_uint32, _c_p]),
@@ -815,7 +816,9 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                              stream=None) -> torch.Tensor:
     """sbn_bitlinear_grouped_grad_w: dW of every expert (bf16 [E, N_out, K]),
-    zero for an expert without rows."""
+    zero for an expert without rows. A workspace given by the caller decides
+    between two parts of dY s / 127 (22 bits of every term, as without one) and
+    one (11 bits, half the MMAs), by its size."""
     _need(dy, torch.bfloat16, "dy")
     _need(xq, torch.int8, "xq")
     rows, n_out = dy.shape
@@ -830,7 +833,7 @@ def bitlinear_grouped_grad_w(dy: torch.Tensor, xq: torch.Tensor, s: torch.Tensor
         out = _new((experts, n_out, k), torch.bfloat16, dy, stream)
     if rows == 0:
         return _zero(out, stream)
-    need = int(lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, experts, k, n_out))
+    need = int(lib().sbn_bitlinear_grouped_grad_w2_workspace_bytes(rows, experts, k, n_out))
     ws = _scratch(need, workspace, dy, stream)
     _run_on(dy.device, "sbn_bitlinear_grouped_grad_w", stream, _ptr(dy), _ptr(xq), _ptr(s), rows, _ptr(offsets),
             experts, k, n_out, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel())

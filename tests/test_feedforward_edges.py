@@ -326,11 +326,13 @@ def test_canaries_of_gradient_workspaces(sbn_lib, cuda_ok, k, n_out, n, m, sizes
     z = torch.randn(rows, n_out, device="cuda", generator=g).to(torch.bfloat16)
     gd = Guarded()
     need_x = int(sbn.lib().sbn_bitlinear_grouped_grad_x_workspace_bytes(rows, n_out))
-    need_w = int(sbn.lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, E, k, n_out))
-    assert (need_x > 0) == (n_out % 8 != 0) and need_w > 0
+    need_w = int(sbn.lib().sbn_bitlinear_grouped_grad_w2_workspace_bytes(rows, E, k, n_out))
+    need_w1 = int(sbn.lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, E, k, n_out))
+    assert (need_x > 0) == (n_out % 8 != 0) and need_w > need_w1 > 0
     dx, dw = gd.tensor((rows, k), torch.bfloat16), gd.tensor((E, n_out, k), torch.bfloat16)
     sbn.bitlinear_grouped_grad_x(dy, o, layer.packed, out=dx, workspace=gd.tensor((need_x,), torch.uint8) if need_x else None)
     sbn.bitlinear_grouped_grad_w(dy, q, s, o, out=dw, workspace=gd.tensor((need_w,), torch.uint8))
+    sbn.bitlinear_grouped_grad_w(dy, q, s, o, out=gd.tensor((E, n_out, k), torch.bfloat16), workspace=gd.tensor((need_w1,), torch.uint8))
     need = sbn.bitlinear_workspace_bytes(rows, k, n_out)
     sbn.bitlinear_act(q, s, layer.packed.expert(0), act="silu", residual=dy, out=gd.tensor((rows, n_out), torch.bfloat16),
                       out_z=gd.tensor((rows, n_out), torch.bfloat16), workspace=gd.tensor((need,), torch.uint8) if need else None)
@@ -534,3 +536,60 @@ def test_two_streams_at_once(sbn_lib, cuda_ok):
         assert all(torch.equal(a, b) for x, y in zip(w, g) for a, b in zip(x, y))
     for a, b in zip(alone, both):
         assert torch.equal(a.params[0], b.params[0]) and torch.equal(a.v[0].float(), b.v[0].float())
+
+
+def test_grouped_dw_workspace_of_two_parts(sbn_lib):
+    """The second part of dY s / 127 adds an fp16 array of the padded rows."""
+    lib = sbn_lib
+    for rows, e, k, n_out in ((64, 4, 256, 64), (64, 4, 256, 65), (1000, 16, 896, 1000), (3, 1024, 128, 9)):
+        one, two = (f(rows, e, k, n_out) for f in (lib.sbn_bitlinear_grouped_grad_w_workspace_bytes,
+                                                   lib.sbn_bitlinear_grouped_grad_w2_workspace_bytes))
+        padded, pitch = (rows + 63 * min(e, rows)) // 64 * 64, -(-n_out // 8) * 8
+        assert two - one == padded * pitch * 2
+    assert lib.sbn_bitlinear_grouped_grad_w2_workspace_bytes(64, 4, 100, 64) == 0
+    assert lib.sbn_bitlinear_grouped_grad_w2_workspace_bytes(0, 4, 128, 64) == 0
+
+
+@gpu
+@pytest.mark.parametrize("n_out", [264, 129])
+@pytest.mark.parametrize("spread", [0, 9])
+def test_grouped_dw_of_terms_that_cancel(sbn_lib, cuda_ok, n_out, spread):
+    """Pairs of rows with opposite gradients and nearly the same activations
+    (as two answers to one prompt have them): dW is what is left of them.
+    Tolerance, u = 2^-24, n rows: a = dY s / 127 carries two roundings in fp32
+    and 2^-22 of itself from its two fp16 parts (half a step of each), or 2^-39 of
+    its column's largest; 2 n exact products summed in fp32 in any order, doubled
+    for the tensor core's alignment of addends, 4 n u of the sum of |products|;
+    one rounding to bf16. One fp16 part, which loses 2^-11 of every term, is 20
+    times over it, but stays within dw_reference's tolerance."""
+    sbn = _sbn()
+    k, sizes = 384, (16, 0, 2, 12, 34)
+    o, spans = run_spans(sizes)
+    rows = sum(sizes)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(rows, k, device="cuda", generator=g)
+    x[1::2] = x[0::2] * (1 + 2.0 ** -6)
+    dy = torch.randn(rows // 2, n_out, device="cuda", generator=g)
+    dy = dy * torch.exp2(spread * torch.rand(rows // 2, n_out, device="cuda", generator=g))
+    dy = torch.stack([dy, -dy], dim=1).view(rows, n_out).to(torch.bfloat16)
+    q, s = sbn.quantize_acts(x.to(torch.bfloat16))
+    xd = q.double() * s.double()[:, None] / 127
+    one = torch.empty(int(sbn.lib().sbn_bitlinear_grouped_grad_w_workspace_bytes(rows, len(sizes), k, n_out)), dtype=torch.uint8,
+                      device="cuda")
+    two_parts = sbn.bitlinear_grouped_grad_w(dy, q, s, o)
+    one_part = sbn.bitlinear_grouped_grad_w(dy, q, s, o, workspace=one)
+    clean(sbn)
+    worst = 0.0
+    for e, (a, b) in enumerate(spans):
+        d, n = dy[a:b].double(), b - a
+        ref, tol = dw_reference(d, xd[a:b])
+        close(one_part[e], ref, tol, f"one part {e}")
+        mag = d.abs().T @ xd[a:b].abs()
+        err = ((4 * n + 10) * U + 2.0 ** -22) * mag
+        if n:
+            err = err + 2.0 ** -39 * d.abs().amax(dim=0)[:, None] * xd[a:b].abs().amax() * n
+        tol = H * ref.abs() + (1 + H) * err
+        close(two_parts[e], ref, tol, f"two parts {e}")
+        if n:
+            worst = max(worst, float(((one_part[e].double() - ref).abs() / tol).max()))
+    assert worst > 3   # the case tells the two apart
