@@ -20,9 +20,9 @@
 // Measured, captured calls: 6.1 us for one token (layer of 6912 x 2560, 6:8, 5.5
 // MB), of which launch, prologue and selector tables are about 4; 9.7 us for 8
 // rows of 8 of 64 experts (K = 2048, N_out = 1408, 7.3 MB). What bounds the
-// latter: 8 rows are quantized by every CTA, and the partial sums of 8 times as
-// many outputs per weight go through shared-memory atomics (stalls on the
-// shared-memory pipe first, 47 % of the issue slots taken, DRAM 6 % busy).
+// latter: every CTA quantizes all 8 rows, and codes, keep bits, selectors,
+// activations and partial sums all pass through shared memory (stalls on its
+// pipe come first; 47 % of the issue slots taken, DRAM 6 % busy).
 #pragma once
 
 #include "async.cuh"
