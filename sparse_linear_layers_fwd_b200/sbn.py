@@ -895,11 +895,9 @@ class AdamW:
             _one_device(self.params[0], *self.copies)
         self._sizes = [p.numel() for p in self.params]
         self._kept = self.params + (self.copies or [])
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in self._kept if t.numel())
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("parameters or copies overlap, or one appears twice")
         self._bytes = [t.nbytes for t in self._kept]
-        self._at = None   # their addresses at the last step
+        self._at = array.array("q", map(torch.Tensor.data_ptr, self._kept))   # their addresses at the last step
+        self._need_apart(self._at)
         # entries of sbn_adamw_tensor: eight 64-bit words each
         self._table = array.array("q", bytes(64 * len(self.params)))
         self._table[7::8] = array.array("q", self._sizes)
@@ -909,6 +907,11 @@ class AdamW:
         if state_bits == 8:
             self.m_scales, self.v_scales = (self._filled(like.new_ones, torch.float32, self._scale_sizes()) for _ in "mv")
         self.step_state = like.new_zeros(2, dtype=torch.int32)
+
+    def _need_apart(self, at) -> None:
+        spans = sorted((a, a + n) for a, n in zip(at, self._bytes) if n)
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters or copies overlap, or one appears twice")
 
     @staticmethod
     def _filled(new, dtype, sizes) -> list:
@@ -1002,7 +1005,9 @@ class AdamW:
         if (list(map(_nbytes, kept)) != self._bytes or not all(map(torch.Tensor.is_contiguous, kept))
                 or at != self._at and any(t.device != self.device for t in kept)):
             raise ValueError("a parameter or a copy changed its size, layout or device")
-        self._at = at
+        if at != self._at:
+            self._need_apart(at)
+            self._at = at
         n = len(self.params)
         table[0::8] = at[:n]
         table[1::8] = array.array("q", map(ptr, grads))

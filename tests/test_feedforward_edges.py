@@ -593,3 +593,24 @@ def test_grouped_dw_of_terms_that_cancel(sbn_lib, cuda_ok, n_out, spread):
         if n:
             worst = max(worst, float(((one_part[e].double() - ref).abs() / tol).max()))
     assert worst > 3   # the case tells the two apart
+
+
+@gpu
+def test_adamw_refuses_storage_exchanged_for_one_in_use(sbn_lib, cuda_ok):
+    """Two parameters whose storage became one, before the first step or later,
+    would be updated by two threads at once."""
+    sbn = _sbn()
+    a, b = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    g = [torch.ones(300, device="cuda"), torch.ones(300, device="cuda")]
+    for steps in (0, 1):
+        opt = sbn.AdamW([a, b])
+        for _ in range(steps):
+            opt.step(g)
+        own, b.data = b.data, a.data
+        with pytest.raises(ValueError):
+            opt.step(g)
+        b.data = torch.ones(900, device="cuda")[10:310]   # one of its own is followed
+        opt.step(g)
+        clean(sbn)
+        assert opt.step_state.tolist() == [steps + 1, 0] and bool((b < 1).all())
+        b.data = own
