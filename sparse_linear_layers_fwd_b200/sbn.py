@@ -895,7 +895,7 @@ class AdamW:
             _one_device(self.params[0], *self.copies)
         self._sizes = [p.numel() for p in self.params]
         self._kept = self.params + (self.copies or [])
-        self._bytes = [t.nbytes for t in self._kept]
+        self._bytes, self._dtypes = [t.nbytes for t in self._kept], [t.dtype for t in self._kept]
         self._at = array.array("q", map(torch.Tensor.data_ptr, self._kept))   # their addresses at the last step
         self._need_apart(self._at)
         # entries of sbn_adamw_tensor: eight 64-bit words each
@@ -1003,8 +1003,8 @@ class AdamW:
         table, ptr, kept = self._table, torch.Tensor.data_ptr, self._kept
         at = array.array("q", map(ptr, kept))
         if (list(map(_nbytes, kept)) != self._bytes or not all(map(torch.Tensor.is_contiguous, kept))
-                or at != self._at and any(t.device != self.device for t in kept)):
-            raise ValueError("a parameter or a copy changed its size, layout or device")
+                or at != self._at and any((t.device, t.dtype) != (self.device, d) for t, d in zip(kept, self._dtypes))):
+            raise ValueError("a parameter or a copy changed its size, type, layout or device")
         if at != self._at:
             self._need_apart(at)
             self._at = at

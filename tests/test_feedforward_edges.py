@@ -614,3 +614,19 @@ def test_adamw_refuses_storage_exchanged_for_one_in_use(sbn_lib, cuda_ok):
         clean(sbn)
         assert opt.step_state.tolist() == [steps + 1, 0] and bool((b < 1).all())
         b.data = own
+
+
+@gpu
+def test_adamw_refuses_storage_of_another_type(sbn_lib, cuda_ok):
+    """Types of as many bytes: fp32 read as bf16 pairs or whole numbers."""
+    sbn = _sbn()
+    p, g = torch.ones(300, device="cuda"), [torch.ones(300, device="cuda")]
+    opt = sbn.AdamW([p])
+    for other in (torch.ones(600, device="cuda", dtype=torch.bfloat16), torch.ones(300, device="cuda", dtype=torch.int32)):
+        p.data = other
+        with pytest.raises(ValueError):
+            opt.step(g)
+    p.data = torch.ones(300, device="cuda")
+    opt.step(g)
+    clean(sbn)
+    assert bool((p < 1).all())
